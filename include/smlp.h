@@ -216,6 +216,115 @@ int shared_mlp_forward_rank(const void* x, const void* w_gate_up, const void* w_
 int shared_mlp_rms_rescale(const float* in, void* out, int64_t M, int64_t H,
                            hipStream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The routed half of the layer: routing to experts, the 8-bit block-scaled product, the
+ * routed experts' SwiGLU.
+ * ------------------------------------------------------------------------------------- */
+
+#define SMLP_MAX_EXPERTS 1024
+#define SMLP_MAX_TOPK 64
+#define SMLP_MAX_GROUPS 64
+
+enum { SMLP_SCORE_SIGMOID = 0, SMLP_SCORE_SOFTMAX = 1 };
+
+/* How shared_mlp_route chooses. */
+typedef struct {
+  int score;       /* SMLP_SCORE_*                                                        */
+  int groups;      /* equal contiguous groups of experts (1 = none)                       */
+  int top_groups;  /* groups that stay eligible, 1 .. groups                              */
+  int group_top;   /* a group counts as the sum of this many largest choices (1 or 2)     */
+  int topk;        /* experts per token                                                   */
+  int renormalize; /* nonzero: weights divided by their sum                               */
+  float scale;     /* factor on the weights                                               */
+} smlp_route;
+
+/*
+ * Routing of tokens to experts.  For row t, with l = fp32(logits[t, :]):
+ *   score   sigmoid: s_e = 1 / (1 + e^-l_e); softmax: s_e = e^(l_e - max l) / sum (a row of
+ *           -inf only: all 0)
+ *   choice  c_e = s_e + bias_e (bias NULL: 0); softmax without a bias: c_e = l_e, the same
+ *           order.  A NaN choice counts below -inf.
+ *   groups  the top_groups groups with the largest sums of their group_top best choices
+ *   ids     the topk eligible experts of largest choice, in descending order
+ *   weights their scores; renormalize: over their sum (0 where it is 0); times scale
+ * Ties go to the lower index everywhere.  Scores, choices and sums are fp32.
+ *   logits  T rows of E elements, row t at logits + t * ldl; dtype SMLP_BF16 or SMLP_FP32
+ *   bias    [E] fp32 or NULL
+ *   ids     [T, topk] int32, weights [T, topk] fp32
+ * E in [1, SMLP_MAX_EXPERTS] and a multiple of groups; topk in [1, SMLP_MAX_TOPK] and at
+ * most top_groups * E / groups; group_top <= E / groups; softmax with group_top 2 needs a
+ * bias (SMLP_ERR_ARG otherwise); ldl >= E; T * max(ldl, topk) < 2^31.  T == 0 is a no-op.
+ */
+int shared_mlp_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ldl, const float* bias,
+                     const smlp_route* route, int32_t* ids, float* weights, hipStream_t stream);
+
+/*
+ * The 8-bit form of a tensor: e4m3 values (OCP, largest finite value 448) with one fp32
+ * scale per group, the value being q * scale.  With a = max(max|x| over the group, 1e-30):
+ *   scale = a / 448,   q = e4m3_rne(x * (448 / a))        (each operation rounded to fp32)
+ * A NaN stays a NaN; an infinity makes every product with its group a NaN.
+ *   x       parts * rows rows of cols elements, row stride ldx; dtype SMLP_BF16 or
+ *           SMLP_FP32; 16-byte aligned, ldx * element size a multiple of 16
+ *   block_rows  1 (activations): groups of 1 row x 128 columns, scales [parts * rows,
+ *           ceil(cols / 128)]; 128 (weights): blocks of 128 rows x 128 columns that start
+ *           anew with each part, scales [parts, ceil(rows / 128), ceil(cols / 128)]
+ *   q       dense [parts * rows, cols], 16-byte aligned
+ * cols a positive multiple of 16; rows >= 1; parts * rows * max(ldx, cols) < 2^40 and at
+ * most 2^31 - 1 blocks.  parts == 0 is a no-op.  (Merged gate_up weights of E experts are
+ * 2 E parts of I rows, down weights E parts of H rows.)
+ */
+int shared_mlp_quant_fp8(const void* x, int dtype, int64_t parts, int64_t rows, int64_t cols, int64_t ldx,
+                         int block_rows, void* q, float* scales, hipStream_t stream);
+
+/* Bytes of workspace shared_mlp_linear_fp8 needs (host-only; x_fp8: x is given as e4m3). */
+int shared_mlp_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t N, int x_fp8, size_t* bytes);
+
+/*
+ * y[m, n] = sum_b xs[m, b] ws[n / 128, b] sum_{k in block b} xq[m, k] wq[n, k], blocks b of
+ * 128 K elements; fp32 accumulation.
+ *   x         x_scales given: e4m3 [M, K] with x_scales [M, ceil(K / 128)]; x_scales NULL:
+ *             bf16 [M, K], brought to that form first (as shared_mlp_quant_fp8 does)
+ *   w         e4m3 [N, K], w_scales [ceil(N / 128), ceil(K / 128)]
+ *   y         M rows of N elements, row m at y + m * ldy; bf16 (out_fp32 == 0, rounded once)
+ *             or fp32 (out_fp32 == 1)
+ * K a positive multiple of 16; N >= 1; ldy >= N; M * K, N * K and M * ldy < 2^31; x and w
+ * 16-byte aligned, y aligned to its element; workspace 256-byte aligned (may be NULL when
+ * 0 bytes are needed).  y must not overlap an input or the workspace.  M == 0 is a no-op.
+ */
+int shared_mlp_linear_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* y,
+                          int64_t M, int64_t K, int64_t N, int64_t ldy, int out_fp32, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace shared_mlp_experts_fp8 needs for these sizes (host-only). */
+int shared_mlp_experts_fp8_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk,
+                                           int partial_fp32, size_t* bytes);
+
+/*
+ * The routed experts' SwiGLU on 8-bit weights, over ids and weights of shared_mlp_route:
+ *   xq = 8-bit form of x (rows in groups of 128);  for each pair (t, j) with
+ *   e = ids[t, j] - first_expert in [0, E):
+ *     g = xq[t] Wg_e^T,  u = xq[t] Wu_e^T,  h = SiLU(g) * u (fp32), hq = 8-bit form of h
+ *     y = hq Wd_e^T
+ *   out[t] = sum_j weights[t, j] * y      (pairs of other experts add nothing; 0 if none)
+ * first_expert and E select the experts this rank holds (expert parallelism); with an
+ * intermediate slice of every expert it is the tensor-parallel partial.
+ *   x           [T, H] bf16
+ *   ids         [T, topk] int32 (any values), weights [T, topk] fp32
+ *   w_gate_up   e4m3 [E, 2 I, H] (gate rows, then up rows), s_gate_up [E, 2 ceil(I / 128),
+ *               ceil(H / 128)]: the row blocks of the gate rows, then those of the up rows
+ *   w_down      e4m3 [E, H, I], s_down [E, ceil(H / 128), ceil(I / 128)]
+ *   out         [T, H] bf16 (rounded once; each expert's y may be rounded to bf16 before the
+ *               fp32 sum where the tiled kernels run) or fp32 (partial_fp32 != 0)
+ *   workspace   >= shared_mlp_experts_fp8_workspace_bytes(...), 256-byte aligned
+ * H and I positive multiples of 16; E in [1, SMLP_MAX_EXPERTS]; topk in [1, SMLP_MAX_TOPK];
+ * T * H, T * topk, T * topk * I and 2 * I * H < 2^31; x, w_gate_up, w_down and out 16-byte
+ * aligned.  out must not overlap an input or the workspace.  T == 0 is a no-op.
+ */
+int shared_mlp_experts_fp8(const void* x, const int32_t* ids, const float* weights, const void* w_gate_up,
+                           const float* s_gate_up, const void* w_down, const float* s_down, void* out, int64_t T,
+                           int64_t H, int64_t I, int64_t E, int64_t topk, int64_t first_expert, int partial_fp32,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -36,6 +36,11 @@ class SmlpError(RuntimeError):
         self.detail = detail
 
 
+class _Route(ctypes.Structure):
+    _fields_ = [("score", _int), ("groups", _int), ("top_groups", _int), ("group_top", _int), ("topk", _int),
+                ("renormalize", _int), ("scale", ctypes.c_float)]
+
+
 class _Plan(ctypes.Structure):
     _fields_ = [("path", _int), ("h_dtype", _int), ("h_offset", _sz), ("workspace_bytes", _sz),
                 ("gate_up_ksplit", _int), ("down_ksplit", _int), ("gate_up_blocks", _int),
@@ -56,6 +61,13 @@ EXPORTS = {
     "shared_mlp_slice_rank": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _vp]),
     "shared_mlp_rms_rescale": (_int, [_vp, _vp, _i64, _i64, _vp]),
     "shared_mlp_forward_rank": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _int, _vp, _sz, _vp]),
+    "shared_mlp_route": (_int, [_vp, _int, _i64, _i64, _i64, _vp, ctypes.POINTER(_Route), _vp, _vp, _vp]),
+    "shared_mlp_quant_fp8": (_int, [_vp, _int, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp]),
+    "shared_mlp_linear_fp8_workspace_bytes": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_sz)]),
+    "shared_mlp_linear_fp8": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp, _sz, _vp]),
+    "shared_mlp_experts_fp8_workspace_bytes": (_int, [_i64, _i64, _i64, _i64, _i64, _int, ctypes.POINTER(_sz)]),
+    "shared_mlp_experts_fp8": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _int,
+                                      _vp, _sz, _vp]),
     # declared in include/smlp_latent.h
     "shared_mlp_linear_plan": (_int, [_i64, _i64, _i64, ctypes.POINTER(_Plan)]),
     "shared_mlp_linear_workspace_bytes": (_int, [_i64, _i64, _i64, ctypes.POINTER(_sz)]),
@@ -444,6 +456,168 @@ def shared_mlp_forward_rank(x, w_gate_up, w_down, out, tp: int, rank: int, works
                                          int(rank), dt, _ptr(workspace), _ws_bytes(workspace),
                                          _stream(stream, x.device)))
     return out
+
+
+# The routed half of the layer (include/smlp.h): routing, the 8-bit block-scaled product, the
+# routed experts.
+
+FP8 = torch.float8_e4m3fn
+ROUTE_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def _typed(name, t, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _blocks128(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _out2d(name, t, rows, cols):
+    """Row stride of an output whose rows are contiguous."""
+    if tuple(t.shape) != (rows, cols) or not t.is_cuda or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a [{rows}, {cols}] GPU tensor with unit column stride")
+    return t.stride(0) if rows > 1 else cols
+
+
+def shared_mlp_route(logits, ids, weights, score="sigmoid", bias=None, groups=1, top_groups=None, group_top=1,
+                     renormalize=True, scale=1.0, stream=None):
+    """Experts and weights of each row of logits [T, E] (bf16 or fp32, unit column stride);
+    ids [T, topk] int32 and weights [T, topk] fp32 are written."""
+    T, E = logits.shape
+    topk = ids.shape[1]
+    ldl = _out2d("logits", logits, T, E)
+    _typed("ids", ids, torch.int32, (T, topk))
+    _typed("weights", weights, torch.float32, (T, topk))
+    if bias is not None:
+        _typed("bias", bias, torch.float32, (E,))
+    _same_device(logits, ids, weights, bias)
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score {score!r} is not one of {sorted(ROUTE_SCORES)}")
+    r = _Route(ROUTE_SCORES[score], int(groups), int(groups if top_groups is None else top_groups), int(group_top),
+               topk, int(bool(renormalize)), float(scale))
+    _check(lib().shared_mlp_route(logits.data_ptr(), _dtype_code(logits), T, E, ldl, _ptr(bias), ctypes.byref(r),
+                                  _ptr(ids), _ptr(weights), _stream(stream, logits.device)))
+
+
+def route(logits, topk: int, score="sigmoid", bias=None, groups=1, top_groups=None, group_top=1, renormalize=True,
+          scale=1.0, stream=None):
+    """Allocating form of shared_mlp_route; returns ids, weights."""
+    ids = torch.empty(logits.shape[0], topk, dtype=torch.int32, device=logits.device)
+    weights = torch.empty(logits.shape[0], topk, dtype=torch.float32, device=logits.device)
+    shared_mlp_route(logits, ids, weights, score, bias, groups, top_groups, group_top, renormalize, scale, stream)
+    return ids, weights
+
+
+def shared_mlp_quant_fp8(x, q, scales, block_rows=1, stream=None):
+    """8-bit form of x [rows, cols] or [parts, rows, cols] (bf16 or fp32, rows equally spaced)."""
+    parts, rows, cols = x.shape if x.dim() == 3 else (1, *x.shape)
+    if not x.is_cuda or x.stride(-1) != 1 or (x.dim() == 3 and parts > 1 and x.stride(0) != rows * x.stride(1)):
+        raise ValueError("x must be a GPU tensor of equally spaced rows with unit column stride")
+    _typed("q", q, FP8, x.shape)
+    lead = (parts,) if x.dim() == 3 else ()
+    _typed("scales", scales, torch.float32,
+           (*lead, rows if block_rows == 1 else _blocks128(rows), _blocks128(cols)))
+    _same_device(x, q, scales)
+    ldx = x.stride(-2) if parts * rows > 1 else cols
+    if rows == 0:
+        return
+    _check(lib().shared_mlp_quant_fp8(x.data_ptr(), _dtype_code(x), parts, rows, cols, ldx, int(block_rows), _ptr(q),
+                                      _ptr(scales), _stream(stream, x.device)))
+
+
+def quantize_fp8(x, block_rows=1, stream=None):
+    """Allocating form of shared_mlp_quant_fp8; returns q, scales."""
+    q = torch.empty(x.shape, dtype=FP8, device=x.device)
+    rows = x.shape[-2] if block_rows == 1 else _blocks128(x.shape[-2])
+    scales = torch.empty(*x.shape[:-2], rows, _blocks128(x.shape[-1]), dtype=torch.float32, device=x.device)
+    shared_mlp_quant_fp8(x, q, scales, block_rows, stream)
+    return q, scales
+
+
+def shared_mlp_linear_fp8_workspace_bytes(M: int, K: int, N: int, x_fp8: bool) -> int:
+    b = _sz()
+    _check(lib().shared_mlp_linear_fp8_workspace_bytes(M, K, N, int(bool(x_fp8)), ctypes.byref(b)))
+    return b.value
+
+
+def shared_mlp_linear_fp8(x, w, w_scales, y, x_scales=None, workspace=None, stream=None):
+    """y = x w^T on 8-bit block-scaled weights [N, K]; x is bf16 [M, K], or e4m3 with
+    x_scales [M, ceil(K / 128)]; y bf16 or fp32 [M, N], unit column stride."""
+    M, K = x.shape
+    N = w.shape[0]
+    _typed("x", x, torch.bfloat16 if x_scales is None else FP8, (M, K))
+    _typed("w", w, FP8, (N, K))
+    _typed("w_scales", w_scales, torch.float32, (_blocks128(N), _blocks128(K)))
+    if x_scales is not None:
+        _typed("x_scales", x_scales, torch.float32, (M, _blocks128(K)))
+    ldy = _out2d("y", y, M, N)
+    if y.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"y dtype {y.dtype} is neither bfloat16 nor float32")
+    _same_device(x, x_scales, w, w_scales, y, workspace)
+    if workspace is None:
+        need = shared_mlp_linear_fp8_workspace_bytes(M, K, N, x_scales is not None)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    _check(lib().shared_mlp_linear_fp8(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), y.data_ptr(), M, K, N, ldy,
+                                       int(y.dtype == torch.float32), _ptr(workspace), _ws_bytes(workspace),
+                                       _stream(stream, x.device)))
+    return y
+
+
+def linear_fp8(x, w, w_scales, x_scales=None, out_fp32=False, workspace=None, stream=None):
+    """Allocating form of shared_mlp_linear_fp8."""
+    y = torch.empty(x.shape[0], w.shape[0], dtype=torch.float32 if out_fp32 else torch.bfloat16, device=x.device)
+    return shared_mlp_linear_fp8(x, w, w_scales, y, x_scales, workspace, stream)
+
+
+def shared_mlp_experts_fp8_workspace_bytes(T: int, H: int, I: int, E: int, topk: int, partial_fp32=False) -> int:
+    b = _sz()
+    _check(lib().shared_mlp_experts_fp8_workspace_bytes(T, H, I, E, topk, int(bool(partial_fp32)), ctypes.byref(b)))
+    return b.value
+
+
+def shared_mlp_experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, out, first_expert=0, workspace=None,
+                           stream=None):
+    """The routed experts' SwiGLU over ids and weights of shared_mlp_route; out [T, H] bf16,
+    or fp32 for a partial.  Experts first_expert .. first_expert + E - 1 are held here."""
+    T, H = x.shape
+    E, _, I = w_down.shape
+    topk = ids.shape[1]
+    _typed("x", x, torch.bfloat16, (T, H))
+    _typed("ids", ids, torch.int32, (T, topk))
+    _typed("weights", weights, torch.float32, (T, topk))
+    _typed("w_gate_up", w_gate_up, FP8, (E, 2 * I, H))
+    _typed("s_gate_up", s_gate_up, torch.float32, (E, 2 * _blocks128(I), _blocks128(H)))
+    _typed("w_down", w_down, FP8, (E, H, I))
+    _typed("s_down", s_down, torch.float32, (E, _blocks128(H), _blocks128(I)))
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out dtype {out.dtype} is neither bfloat16 nor float32")
+    _typed("out", out, out.dtype, (T, H))
+    _same_device(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, out, workspace)
+    partial = out.dtype == torch.float32
+    if workspace is None:
+        need = shared_mlp_experts_fp8_workspace_bytes(T, H, I, E, topk, partial)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+    _check(lib().shared_mlp_experts_fp8(_ptr(x), _ptr(ids), _ptr(weights), _ptr(w_gate_up), _ptr(s_gate_up),
+                                        _ptr(w_down), _ptr(s_down), _ptr(out), T, H, I, E, topk, int(first_expert),
+                                        int(partial), _ptr(workspace), _ws_bytes(workspace),
+                                        _stream(stream, x.device)))
+    return out
+
+
+def experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert=0, partial_fp32=False,
+                workspace=None, stream=None):
+    """Allocating form of shared_mlp_experts_fp8."""
+    out = torch.empty(x.shape, dtype=torch.float32 if partial_fp32 else torch.bfloat16, device=x.device)
+    return shared_mlp_experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, out, first_expert, workspace,
+                                  stream)
 
 
 # Measurement kernels (include/smlp_ceilings.h): launch them, time them on the caller's side.

@@ -21,7 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsmlp.so")
 
 SOURCES = ["api.cpp", "layout.cpp", "skinny.hip", "gemm.hip", "aux.hip", "latent.hip", "ceilings.hip",
-           "noalloc.hip"]
+           "noalloc.hip", "moe.cpp", "route.hip", "fp8.hip"]
 ARCH = "gfx950"
 
 

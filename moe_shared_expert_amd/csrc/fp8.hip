@@ -1,0 +1,918 @@
+// 8-bit (e4m3) block-scaled products: the plain projection and the two products of the
+// routed experts, and the kernels around them (quantisation, the sort of token-expert
+// pairs, the weighted sum of a token's experts).
+//
+// y[m, n] = sum_b as[m, b] ws[n / 128, b] sum_{k in block b} a[m, k] w[n, k]
+//
+// b runs over blocks of 128 K elements.  One 16x16x128 matrix instruction multiplies
+// exactly one block of a 16 x 16 output tile, starting from zero; its four results per lane
+// are then added into fp32 accumulators with one multiply-add each, scaled by as * ws.  The
+// weights are the instruction's A operand, so a lane holds one token's results (one
+// activation scale per lane and tile) for four consecutive output features (one 8- or
+// 16-byte store), and the weight scale is the same for the whole wave.
+//
+// Operands reach LDS by direct loads in 1 KB blocks of 8 rows x 128 bytes, the 16-byte
+// chunks of a row permuted so that the fragment reads are free of bank conflicts.  The
+// scales of a K block travel the same way, as one 4-byte-per-lane load beside the data.
+//
+// The streaming kernel, every product that is returned in fp32 and projections of at most four
+// blocks go through the bf16 instructions (exact products, fp32 sums); the tiled kernel with
+// bf16 results uses the 8-bit instruction at twice the rate, whose error of about 1.4e-5 of a
+// block's sum is far below the rounding of the result.
+#include "fp8.h"
+#include "internal.h"
+#include "smlp.h"
+
+namespace smlp {
+
+namespace {
+
+enum { F8_LINEAR = 0, F8_GATE_UP = 1, F8_DOWN = 2 };
+
+struct F8Args {
+  const uint8_t* a;    // activations [rows, K]
+  uint32_t a_bytes;
+  const float* as;     // scale of activation row r, block b: as[r * as_row + b * as_kb]
+  int as_row, as_kb;
+  const uint8_t* w;    // weights of expert e at w + e * w_stride, rows of K bytes
+  size_t w_stride;
+  uint32_t w_bytes;    // bytes of one expert's weights
+  const float* ws;     // block scales of expert e at ws + e * ws_stride, rows of KB
+  size_t ws_stride;
+  int K, KB;           // K elements and blocks of 128
+  int N;               // features (gate_up: of h)
+  int nblk;            // 128-row blocks of N
+  int M;               // projection: rows of a
+  int tiles_m, tiles_n;
+  const int* hdr;      // experts: tile list (SortHeader layout below)
+  const int* perm;     // experts: pair at each sorted position
+  int topk;
+  void* out;           // projection: y; gate_up: h; down: y of each pair
+  int ldo;
+  int out_f32;         // fp32 (1) or bf16 (0) output; gate_up: fp32 h (1) or e4m3 h (0)
+  float* hs;           // gate_up with e4m3 h: scales, block b of position p at hs[b * hs_ld + p]
+  int hs_ld;
+  float* part;         // projection with a K split: fp32 partials [slices][M][N]
+  int kslice;          // K blocks per slice
+};
+
+// Tile list of the experts' products: hdr[0] = tiles, then (expert, first sorted position,
+// rows) of each.
+__device__ __forceinline__ bool f8_tile(const F8Args& g, int mode, int bm, int tile, int& expert, int& start,
+                                        int& count) {
+  if (mode == F8_LINEAR) {
+    expert = 0;
+    start = tile * bm;
+    count = min(bm, g.M - start);
+    return true;
+  }
+  if (tile >= g.hdr[0]) return false;
+  expert = g.hdr[4 + tile * 4];
+  start = g.hdr[5 + tile * 4];
+  count = g.hdr[6 + tile * 4];
+  return true;
+}
+
+// Activation row of row r of a tile.
+__device__ __forceinline__ int f8_arow(const F8Args& g, int mode, int start, int r) {
+  if (mode == F8_GATE_UP) return g.perm[start + r] / g.topk;
+  return start + r;
+}
+
+__device__ __forceinline__ void f8_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
+template <int LPS, int MAXL>
+__device__ __forceinline__ void f8_wait_steps(int later) {
+  if constexpr (MAXL == 0) {
+    wait_vmcnt<0>();
+  } else {
+    if (later >= MAXL) wait_vmcnt<MAXL * LPS>();
+    else f8_wait_steps<LPS, MAXL - 1>(later);
+  }
+}
+
+// Store four consecutive features n .. n+3 of one output row.
+__device__ __forceinline__ void f8_store4(const F8Args& g, size_t row, int n, f32x4 v) {
+  const size_t at = row * (size_t)g.ldo + n;
+  if (g.out_f32) {
+    float* p = reinterpret_cast<float*>(g.out) + at;
+    if (n + 3 < g.N && ((uintptr_t)p & 15) == 0) {
+      *reinterpret_cast<f32x4*>(p) = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < g.N) p[j] = v[j];
+    }
+  } else {
+    uint16_t* p = reinterpret_cast<uint16_t*>(g.out) + at;
+    if (n + 3 < g.N && ((uintptr_t)p & 7) == 0) {
+      *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < g.N) p[j] = (uint16_t)f2bf(v[j]);
+    }
+  }
+}
+
+// Weight streaming (few rows per tile).  A workgroup owns NT tiles of 16 weight rows
+// (gate_up: NT / 2 tiles of gate rows and the matching up rows) and one tile of 16 * MT
+// activation rows; its waves take the K blocks in turn, each through a ring of its own, and
+// their sums are added in wave order.
+template <int NT, int MT, int WAVES, int STAGES, int MODE>
+__global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
+  constexpr bool GU = MODE == F8_GATE_UP;
+  constexpr int FT = GU ? NT / 2 : NT;  // feature tiles
+  constexpr int SLOT = (NT + MT) * 2048 + 256;
+  constexpr int LPS = 2 * (NT + MT) + 1;
+  constexpr int RING = WAVES * STAGES * SLOT;
+  constexpr int RED = WAVES * NT * MT * 64 * 16;
+  static_assert(LPS * (STAGES - 1) < 64, "loads in flight");
+  __shared__ __attribute__((aligned(1024))) char lds[RING > RED ? RING : RED];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ln = lane & 15, lg = lane >> 4, lr = lane >> 3;
+  int expert, start, count;
+  if (!f8_tile(g, MODE, 16 * MT, blockIdx.y, expert, start, count)) return;
+  const int f0 = blockIdx.x * (16 * FT);
+  const int K = g.K;
+  const uint8_t* w = g.w + (size_t)expert * g.w_stride;
+  const float* ws = g.ws + (size_t)expert * g.ws_stride;
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(w, g.w_bytes);
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(g.a, g.a_bytes);
+
+  int ch[2];
+  uint32_t wo[NT][2], ao[MT][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    ch[h] = (lane & 7) ^ (((8 * h + lr) >> 1) & 7);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int f = f0 + 16 * (t % FT) + 8 * h + lr;
+      const int row = t < FT ? f : g.N + f;
+      wo[t][h] = f < g.N ? (uint32_t)row * (uint32_t)K + ch[h] * 16 : g.w_bytes;
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int r = 16 * t + 8 * h + lr;
+      ao[t][h] = r < count ? (uint32_t)f8_arow(g, MODE, start, r) * (uint32_t)K + ch[h] * 16 : g.a_bytes;
+    }
+  }
+  // Scale source of this lane: lanes 0 .. 16 MT - 1 the activation rows, lanes 32 and up
+  // the weight blocks (even lanes the gate or only one, odd lanes the up block).
+  const float* sp;
+  int sstep;
+  if (lane < 32) {
+    sp = g.as + (size_t)f8_arow(g, MODE, start, min(lane & (16 * MT - 1), count - 1)) * g.as_row;
+    sstep = g.as_kb;
+  } else {
+    const int blk = min(f0 / 128, g.nblk - 1) + (GU && (lane & 1) ? g.nblk : 0);
+    sp = ws + (size_t)blk * g.KB;
+    sstep = 1;
+  }
+
+  char* my = lds + wave * (STAGES * SLOT);
+  const int nst = (g.KB + WAVES - 1) / WAVES;
+  auto issue = [&](int slot, int i) {
+    const int kb = i * WAVES + wave;
+    const int k = kb * 128;
+    char* sl = my + slot * SLOT;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        buf_ld_lds_nt(wr, sl + t * 2048 + h * 1024,
+                      (k + ch[h] * 16 < K && wo[t][h] != g.w_bytes) ? wo[t][h] + k : g.w_bytes);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        buf_ld_lds(ar, sl + (NT + t) * 2048 + h * 1024,
+                   (k + ch[h] * 16 < K && ao[t][h] != g.a_bytes) ? ao[t][h] + k : g.a_bytes);
+    glb_ld_lds4(sp + (size_t)min(kb, g.KB - 1) * sstep, sl + (NT + MT) * 2048);
+  };
+
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int st = 0; st < STAGES - 1; ++st)
+    if (st < nst) issue(st, st);
+  for (int i = 0; i < nst; ++i) {
+    // The fragments of the slot about to be refilled were all read (and waited for) in the
+    // previous step.
+    if (i + STAGES - 1 < nst) issue((i + STAGES - 1) % STAGES, i + STAGES - 1);
+    f8_wait_steps<LPS, STAGES - 1>(min(STAGES - 1, nst - 1 - i));
+    asm volatile("" ::: "memory");
+    const char* sl = my + (i % STAGES) * SLOT;
+    const float* sc = reinterpret_cast<const float*>(sl + (NT + MT) * 2048);
+    frag_bf16 af[MT];
+    float sg[MT], su[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      af[m] = widen(lds_frag(sl + (NT + m) * 2048, lane));
+      const float s = sc[16 * m + ln];
+      sg[m] = s * sc[32];
+      su[m] = GU ? s * sc[33] : sg[m];
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const frag_bf16 wf = widen(lds_frag(sl + t * 2048, lane));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const f32x4 p = mfma_widened(wf, af[m]);
+        const float s = t < FT ? sg[m] : su[m];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[t][m][j] = fmaf(p[j], s, acc[t][m][j]);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this slot's reads are done
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+  }
+
+  // Add the waves' sums in wave order; wave 0 finishes.
+  if constexpr (WAVES > 1) {
+    f32x4* red = reinterpret_cast<f32x4*>(lds);
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) red[(wave * NT * MT + t * MT + m) * 64 + lane] = acc[t][m];
+    __syncthreads();
+    if (wave != 0) return;
+    for (int v = 1; v < WAVES; ++v)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[t][m] += red[(v * NT * MT + t * MT + m) * 64 + lane];
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int r = 16 * m + ln;
+    if (r >= count) continue;
+#pragma unroll
+    for (int t = 0; t < FT; ++t) {
+      const int n = f0 + 16 * t + 4 * lg;
+      if (n >= g.N) continue;
+      f32x4 v = acc[t][m];
+      size_t row = start + r;
+      if constexpr (GU) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = silu_mul(v[j], acc[t + FT][m][j]);
+      } else if (MODE == F8_DOWN) {
+        row = g.perm[start + r];
+      }
+      f8_store4(g, row, n, v);
+    }
+  }
+}
+
+// Workgroup -> (tile_m, tile_n): each XCD (workgroups are handed out round-robin over the 8)
+// takes a contiguous run of the tiles, walked in groups of GROUP_M row tiles, so that the
+// workgroups resident on one XCD share weight and activation tiles in its L2.
+__device__ __forceinline__ bool f8_coords(int tiles_m, int tiles_n, int lin, int& tm, int& tn) {
+  constexpr int XCDS = 8, GROUP_M = 4;
+  const int total = tiles_m * tiles_n;
+  if (lin >= total) return false;
+  const int per = total / XCDS, rem = total % XCDS;
+  const int xcd = lin % XCDS, idx = lin / XCDS;
+  const int f = xcd * per + min(xcd, rem) + idx;
+  const int group = GROUP_M * tiles_n;
+  const int gi = f / group, first = gi * GROUP_M;
+  const int gsize = min(tiles_m - first, GROUP_M);
+  const int in = f - gi * group;
+  tm = first + in % gsize;
+  tn = in / gsize;
+  return true;
+}
+
+// LDS-tiled kernel: BM activation rows x BN weight rows (gate_up: BN / 2 features and
+// both their rows) per workgroup, WM x WN waves.  EXACT: products through bf16.
+template <int BM, int BN, int WM, int WN, int NS, int MODE, bool EXACT>
+__global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
+  constexpr bool GU = MODE == F8_GATE_UP;
+  constexpr int W = WM * WN;
+  constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
+  constexpr int FT = GU ? TN / 2 : TN;
+  constexpr int FN = GU ? BN / 2 : BN;  // features per workgroup
+  constexpr int AL = BM / 8 / W, BL = BN / 8 / W;
+  constexpr int RPW = BM / W;  // activation rows whose scales a wave fetches
+  static_assert(AL * W * 8 == BM && BL * W * 8 == BN && RPW <= 32, "tile / wave mismatch");
+  static_assert(!GU || (TN % 2 == 0 && FN == 128), "a gate_up workgroup covers one scale group of h");
+  static_assert(BN / WN <= 128 && 128 % (16 * FT) == 0, "one weight scale per wave");
+  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+  constexpr int STAGE = A_BYTES + B_BYTES + W * 256;
+  constexpr int LPS = AL + BL + 1;
+  static_assert(NS >= 2 && LPS * (NS - 1) < 64, "loads in flight");
+  __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  const int ln = lane & 15, lg = lane >> 4, lr = lane >> 3;
+  int tile_m, tile_n, expert, start, count;
+  const int tiles_m = MODE == F8_LINEAR ? g.tiles_m : g.hdr[0];
+  if (!f8_coords(tiles_m, g.tiles_n, blockIdx.x, tile_m, tile_n)) return;
+  if (!f8_tile(g, MODE, BM, tile_m, expert, start, count)) return;
+  const int f0 = tile_n * FN;
+  const int K = g.K;
+  const int kb0 = blockIdx.y * g.kslice;
+  const int nk = min(g.KB - kb0, g.kslice);
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + (size_t)expert * g.w_stride, g.w_bytes);
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(g.a, g.a_bytes);
+
+  // Block i of this wave: tile rows (i * W + wave) * 8 .. + 7.
+  uint32_t aoff[AL], boff[BL];
+  int achk[AL], bchk[BL];
+#pragma unroll
+  for (int i = 0; i < AL; ++i) {
+    const int r = (i * W + wave) * 8 + lr;
+    achk[i] = (lane & 7) ^ ((r >> 1) & 7);
+    aoff[i] = r < count ? (uint32_t)f8_arow(g, MODE, start, r) * (uint32_t)K + achk[i] * 16 : g.a_bytes;
+  }
+#pragma unroll
+  for (int i = 0; i < BL; ++i) {
+    const int r = (i * W + wave) * 8 + lr;
+    bchk[i] = (lane & 7) ^ ((r >> 1) & 7);
+    int f = f0 + r, row = f;
+    if (GU) {
+      // Each wave column's 16 * TN rows: its gate rows, then the matching up rows.
+      const int wc = r / (16 * TN), rr = r % (16 * TN);
+      f = f0 + wc * 16 * FT + rr % (16 * FT);
+      row = rr < 16 * FT ? f : g.N + f;
+    }
+    boff[i] = f < g.N ? (uint32_t)row * (uint32_t)K + bchk[i] * 16 : g.w_bytes;
+  }
+  // Scale source of this lane: lanes 0 .. RPW - 1 activation rows wave * RPW + lane, lanes
+  // 32 and up the block of this wave's weight rows (odd lanes: of its up rows).
+  const float* sp;
+  int sstep;
+  if (lane < 32) {
+    const int r = wave * RPW + lane % RPW;
+    sp = g.as + (size_t)f8_arow(g, MODE, start, min(r, count - 1)) * g.as_row;
+    sstep = g.as_kb;
+  } else {
+    const int blk = min((f0 + wn * 16 * FT) / 128, g.nblk - 1) + (GU && (lane & 1) ? g.nblk : 0);
+    sp = g.ws + (size_t)expert * g.ws_stride + (size_t)blk * g.KB;
+    sstep = 1;
+  }
+
+  auto issue = [&](int buf, int kb) {
+    char* st = lds + buf * STAGE;
+    const int k = kb * 128;
+#pragma unroll
+    for (int i = 0; i < AL; ++i)
+      buf_ld_lds(ar, st + (i * W + wave) * 1024,
+                 (aoff[i] != g.a_bytes && k + achk[i] * 16 < K) ? aoff[i] + k : g.a_bytes);
+#pragma unroll
+    for (int i = 0; i < BL; ++i)
+      buf_ld_lds(wr, st + A_BYTES + (i * W + wave) * 1024,
+                 (boff[i] != g.w_bytes && k + bchk[i] * 16 < K) ? boff[i] + k : g.w_bytes);
+    glb_ld_lds4(sp + (size_t)kb * sstep, st + A_BYTES + B_BYTES + wave * 256);
+  };
+
+  f32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st)
+    if (st < nk) issue(st, kb0 + st);
+  for (int kt = 0; kt < nk; ++kt) {
+    f8_wait_steps<LPS, NS - 2>(min(NS - 2, nk - 1 - kt));
+    f8_barrier();
+    if (kt + NS - 1 < nk) issue((kt + NS - 1) % NS, kb0 + kt + NS - 1);
+    const char* st = lds + (kt % NS) * STAGE;
+    const char* sc = st + A_BYTES + B_BYTES;
+    const float swg = *reinterpret_cast<const float*>(sc + wave * 256 + 128);
+    const float swu = GU ? *reinterpret_cast<const float*>(sc + wave * 256 + 132) : swg;
+    auto frag = [&](const char* tile) {
+      if constexpr (EXACT) return widen(lds_frag(tile, lane));
+      else return lds_frag(tile, lane);
+    };
+    decltype(frag(st)) wf[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) wf[j] = frag(st + A_BYTES + (wn * TN + j) * 2048);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const auto af = frag(st + (wm * TM + i) * 2048);
+      const int r = (wm * TM + i) * 16 + ln;
+      const float s = *reinterpret_cast<const float*>(sc + (r / RPW) * 256 + (r % RPW) * 4);
+      const float sg = s * swg, su = s * swu;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        f32x4 p;
+        if constexpr (EXACT) p = mfma_widened(wf[j], af);
+        else p = mfma_fp8(wf[j], af);
+        const float sj = j < FT ? sg : su;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sj, acc[i][j][e]);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+  }
+
+  if constexpr (GU) {
+    // h = SiLU(gate) * up, then e4m3 with one scale per row and 128 features: the rows'
+    // largest magnitudes over this wave's features, then over the waves of a row.
+    float* red = reinterpret_cast<float*>(lds);
+    f8_barrier();  // every wave has read its last fragments (lgkmcnt 0 above)
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      float mx = 0.f;
+#pragma unroll
+      for (int j = 0; j < FT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = silu_mul(acc[i][j][e], acc[i][j + FT][e]);
+          acc[i][j][e] = v;
+          mx = fmaxf(mx, fabsf(v));
+        }
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      if (lg == 0) red[wn * BM + (wm * TM + i) * 16 + ln] = mx;
+    }
+    __syncthreads();
+    const int blk = f0 / 128;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int r = (wm * TM + i) * 16 + ln;
+      float mx = kAmaxMin;
+#pragma unroll
+      for (int v = 0; v < WN; ++v) mx = fmaxf(mx, red[v * BM + r]);
+      const float inv = kE4M3Max / mx;
+      if (r >= count) continue;
+      if (wn == 0 && lg == 0) g.hs[(size_t)blk * g.hs_ld + start + r] = mx / kE4M3Max;
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        const int n = f0 + wn * 16 * FT + 16 * j + 4 * lg;  // N is a multiple of 16
+        if (n < g.N)
+          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(g.out) + (size_t)(start + r) * g.N + n) =
+              pack_fp8x4(acc[i][j][0] * inv, acc[i][j][1] * inv, acc[i][j][2] * inv, acc[i][j][3] * inv);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int r = (wm * TM + i) * 16 + ln;
+      if (r >= count) continue;
+      const size_t row = MODE == F8_DOWN ? (size_t)g.perm[start + r] : (size_t)(start + r);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int n = f0 + (wn * TN + j) * 16 + 4 * lg;
+        if (n >= g.N) continue;
+        if (MODE == F8_LINEAR && gridDim.y > 1) {
+          float* p = g.part + ((size_t)blockIdx.y * g.M + row) * (size_t)g.N + n;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < g.N) p[e] = acc[i][j][e];
+        } else {
+          f8_store4(g, row, n, acc[i][j]);
+        }
+      }
+    }
+  }
+}
+
+// Sum of the K slices' partials in slice order.
+__global__ __launch_bounds__(256) void f8_join_kernel(const float* part, int slices, int M, int N, void* out,
+                                                      int ldo, int out_f32) {
+  const size_t total = (size_t)M * N;
+  for (size_t e = blockIdx.x * (size_t)256 + threadIdx.x; e < total; e += (size_t)gridDim.x * 256) {
+    float v = part[e];
+    for (int q = 1; q < slices; ++q) v += part[q * total + e];
+    const size_t at = e / N * ldo + e % N;
+    if (out_f32) reinterpret_cast<float*>(out)[at] = v;
+    else reinterpret_cast<uint16_t*>(out)[at] = (uint16_t)f2bf(v);
+  }
+}
+
+// Quantisation of rows in groups of 128 columns: 16 lanes per group, 8 elements each.
+// scale of row r, group b: s[r * s_row + b * s_kb].
+struct QuantArgs {
+  const void* x;
+  int64_t rows;
+  int cols;      // multiple of 16
+  int64_t ldx;
+  int bf16;
+  uint8_t* q;    // dense [rows, cols]
+  float* s;
+  int64_t s_row, s_kb;
+};
+
+// Eight elements at p (16-byte aligned).
+__device__ __forceinline__ void load8(const void* x, size_t at, int bf16, float (&v)[8]) {
+  if (bf16) {
+    const u32x4 u = ld16(reinterpret_cast<const uint16_t*>(x) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf_lo(u[i]);
+      v[2 * i + 1] = bf_hi(u[i]);
+    }
+  } else {
+    const float* p = reinterpret_cast<const float*>(x) + at;
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  }
+}
+
+__device__ __forceinline__ void quant_group(const QuantArgs& a, int64_t group, int KB) {
+  const int l = threadIdx.x & 15;
+  const int64_t row = group / KB;
+  const int b = (int)(group - row * KB);
+  const int c = b * 128 + l * 8;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const bool in = row < a.rows && c < a.cols;
+  if (in) load8(a.x, (size_t)row * a.ldx + c, a.bf16, v);
+  float mx = kAmaxMin;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+  if (!in) return;
+  const float inv = kE4M3Max / mx;
+  *reinterpret_cast<u32x2*>(a.q + (size_t)row * a.cols + c) =
+      u32x2{pack_fp8x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+            pack_fp8x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+  if (l == 0) a.s[row * a.s_row + b * a.s_kb] = mx / kE4M3Max;
+}
+
+__global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
+  const int KB = (a.cols + 127) / 128;
+  const int64_t groups = a.rows * KB;
+  const int64_t step = (int64_t)gridDim.x * 16;
+  // Whole workgroups iterate together: the last round's idle groups read nothing.
+  for (int64_t g = (int64_t)blockIdx.x * 16; g < groups; g += step) quant_group(a, g + (threadIdx.x >> 4), KB);
+}
+
+// Quantisation in 128 x 128 blocks of parts x rows x cols: one workgroup per block.
+__global__ __launch_bounds__(256) void quant_blocks_kernel(QuantArgs a, int rows_per_part) {
+  __shared__ float red[4];
+  const int KB = (a.cols + 127) / 128, RB = (rows_per_part + 127) / 128;
+  const int64_t id = blockIdx.x;
+  const int b = (int)(id % KB);
+  const int64_t rb = id / KB;
+  const int64_t part = rb / RB;
+  const int r0 = (int)(rb % RB) * 128;
+  const int nr = min(128, rows_per_part - r0);
+  const int64_t row0 = part * rows_per_part + r0;
+  const int l = threadIdx.x & 15, rr = threadIdx.x >> 4;
+  const int c = b * 128 + l * 8;
+  float mx = kAmaxMin;
+  for (int r = rr; r < nr; r += 16) {
+    if (c >= a.cols) break;
+    float v[8];
+    load8(a.x, (size_t)(row0 + r) * a.ldx + c, a.bf16, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float inv = kE4M3Max / mx;
+  for (int r = rr; r < nr; r += 16) {
+    if (c >= a.cols) break;
+    float v[8];
+    load8(a.x, (size_t)(row0 + r) * a.ldx + c, a.bf16, v);
+    *reinterpret_cast<u32x2*>(a.q + (size_t)(row0 + r) * a.cols + c) =
+        u32x2{pack_fp8x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+              pack_fp8x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+  }
+  if (threadIdx.x == 0) a.s[(rb * KB) + b] = mx / kE4M3Max;
+}
+
+// Index of expert `id` among the E held from `first` on, or -1.
+__device__ __forceinline__ int local_expert(int id, int first, int E) {
+  return id >= first && id - first < E ? id - first : -1;
+}
+
+// First launch of the experts: workgroup 0 sorts the pairs (token, choice) by expert and
+// writes the tile list; the others quantise x.  Pairs whose expert is outside
+// [first, first + E) are dropped.
+struct PrepArgs {
+  const int32_t* ids;
+  int pairs, E, first, bm;
+  int* hdr;    // [0] tiles, then 4 words per tile
+  int* perm;
+  QuantArgs q;
+};
+
+constexpr int kPrepThreads = 1024;
+
+__global__ __launch_bounds__(kPrepThreads) void experts_prep_kernel(PrepArgs a) {
+  if (blockIdx.x > 0) {
+    const int KB = (a.q.cols + 127) / 128;
+    const int64_t groups = a.q.rows * KB;
+    constexpr int PER = kPrepThreads / 16;
+    const int64_t step = (int64_t)(gridDim.x - 1) * PER;
+    for (int64_t g = (int64_t)(blockIdx.x - 1) * PER; g < groups; g += step)
+      quant_group(a.q, g + (threadIdx.x >> 4), KB);
+    return;
+  }
+  static_assert(SMLP_MAX_EXPERTS <= kPrepThreads, "one thread per expert");
+  __shared__ int count[kPrepThreads], off[kPrepThreads], wsum[2][kPrepThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  count[tid] = 0;
+  __syncthreads();
+  for (int p = tid; p < a.pairs; p += kPrepThreads) {
+    const int e = local_expert(a.ids[p], a.first, a.E);
+    if (e >= 0) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  // Thread e: first sorted position and first tile of expert e, by a scan over the threads.
+  const int c = count[tid], nt = (c + a.bm - 1) / a.bm;
+  int o = c, t = nt;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int uo = __shfl_up(o, d), ut = __shfl_up(t, d);
+    if (lane >= d) {
+      o += uo;
+      t += ut;
+    }
+  }
+  if (lane == 63) {
+    wsum[0][wave] = o;
+    wsum[1][wave] = t;
+  }
+  __syncthreads();
+  for (int v = 0; v < wave; ++v) {
+    o += wsum[0][v];
+    t += wsum[1][v];
+  }
+  if (tid == kPrepThreads - 1) a.hdr[0] = t;
+  off[tid] = o - c;
+  for (int i = 0, q = t - nt; i < c; i += a.bm, ++q) {
+    a.hdr[4 + 4 * q] = tid;
+    a.hdr[5 + 4 * q] = o - c + i;
+    a.hdr[6 + 4 * q] = min(a.bm, c - i);
+  }
+  __syncthreads();
+  // The order within an expert does not change any result (a row's sums do not depend on
+  // its place in a tile); rounds of the workgroup keep it near token order.
+  for (int p0 = 0; p0 < a.pairs; p0 += kPrepThreads) {
+    const int p = p0 + tid;
+    if (p < a.pairs) {
+      const int e = local_expert(a.ids[p], a.first, a.E);
+      if (e >= 0) a.perm[atomicAdd(&off[e], 1)] = p;
+    }
+    __syncthreads();
+  }
+}
+
+// out[t] = sum_j weights[t, j] y[t * topk + j] over the local experts, in fp32.
+struct CombineArgs {
+  const void* y;
+  int y_f32;
+  const int32_t* ids;
+  const float* weights;
+  void* out;
+  int T, H, E, first, topk, out_f32;
+};
+
+__global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
+  const int per = a.H / 8;
+  const int64_t total = (int64_t)a.T * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int t = (int)(i / per), c = (int)(i - (int64_t)t * per) * 8;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < a.topk; ++j) {
+      const int64_t p = (int64_t)t * a.topk + j;
+      if (local_expert(a.ids[p], a.first, a.E) < 0) continue;
+      const float w = a.weights[p];
+      float v[8];
+      load8(a.y, (size_t)p * a.H + c, !a.y_f32, v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+    }
+    const size_t at = (size_t)t * a.H + c;
+    if (a.out_f32) {
+      f32x4* o = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + at);
+      o[0] = f32x4{acc[0], acc[1], acc[2], acc[3]};
+      o[1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
+    } else {
+      *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+          u32x4{pack_bf2(acc[0], acc[1]), pack_bf2(acc[2], acc[3]), pack_bf2(acc[4], acc[5]),
+                pack_bf2(acc[6], acc[7])};
+    }
+  }
+}
+
+unsigned quant_grid(int64_t groups, int per) {
+  const int64_t n = (groups + per - 1) / per;
+  return (unsigned)(n < 1 ? 1 : n > 2048 ? 2048 : n);
+}
+
+template <int MODE>
+int launch_f8(const F8Plan& p, const F8Args& a, int max_tiles, hipStream_t s) {
+  if (p.kind == F8_KIND_STREAM) {
+    const int per = (MODE == F8_GATE_UP ? 8 : 16) * p.nt;
+    const dim3 grid((unsigned)((a.N + per - 1) / per), (unsigned)max_tiles);
+#define SMLP_F8(NT_, MT_, W_, S_)                                                                      \
+  if (p.nt == NT_ && p.mt == MT_ && p.waves == W_ && p.stages == S_) {                                 \
+    hipLaunchKernelGGL((f8_stream_kernel<NT_, MT_, W_, S_, MODE>), grid, dim3(W_ * 64), 0, s, a);      \
+    return (int)hipGetLastError();                                                                     \
+  }
+    SMLP_F8(2, 1, 4, 4) SMLP_F8(2, 2, 4, 4)
+#undef SMLP_F8
+    return (int)hipErrorInvalidConfiguration;
+  }
+  const int fn = MODE == F8_GATE_UP ? p.bn / 2 : p.bn;
+  F8Args g = a;
+  g.tiles_n = (a.N + fn - 1) / fn;
+  g.tiles_m = max_tiles;
+  const dim3 grid((unsigned)(g.tiles_n * max_tiles), (unsigned)p.ksplit);
+#define SMLP_F8(BM_, BN_, WM_, WN_, NS_)                                                               \
+  if (p.bm == BM_ && p.bn == BN_) {                                                                    \
+    if (p.exact)                                                                                       \
+      hipLaunchKernelGGL((f8_tile_kernel<BM_, BN_, WM_, WN_, NS_, MODE, true>), grid,                  \
+                         dim3(WM_ * WN_ * 64), 0, s, g);                                               \
+    else                                                                                               \
+      hipLaunchKernelGGL((f8_tile_kernel<BM_, BN_, WM_, WN_, NS_, MODE, false>), grid,                 \
+                         dim3(WM_ * WN_ * 64), 0, s, g);                                               \
+    return (int)hipGetLastError();                                                                     \
+  }
+  SMLP_F8(64, 256, 1, 4, 3) SMLP_F8(256, 256, 2, 4, 2)
+  if constexpr (MODE != F8_GATE_UP) { SMLP_F8(64, 64, 2, 2, 4) SMLP_F8(128, 128, 2, 2, 3) }
+#undef SMLP_F8
+  return (int)hipErrorInvalidConfiguration;
+}
+
+}  // namespace
+
+int launch_quant_fp8(const void* x, int bf16, int64_t parts, int64_t rows, int64_t cols, int64_t ldx,
+                     int block_rows, void* q, float* scales, int64_t s_row, int64_t s_kb, hipStream_t s) {
+  QuantArgs a{};
+  a.x = x;
+  a.rows = parts * rows;
+  a.cols = (int)cols;
+  a.ldx = ldx;
+  a.bf16 = bf16;
+  a.q = static_cast<uint8_t*>(q);
+  a.s = scales;
+  a.s_row = s_row;
+  a.s_kb = s_kb;
+  const int64_t KB = (cols + 127) / 128;
+  if (block_rows == 1) {
+    hipLaunchKernelGGL(quant_rows_kernel, dim3(quant_grid(a.rows * KB, 16)), dim3(256), 0, s, a);
+  } else {
+    const int64_t blocks = parts * ((rows + 127) / 128) * KB;
+    hipLaunchKernelGGL(quant_blocks_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, (int)rows);
+  }
+  return (int)hipGetLastError();
+}
+
+int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t as_row, int64_t as_kb,
+                      const void* w, const float* ws, void* y, int64_t M, int64_t K, int64_t N, int64_t ldy,
+                      int out_f32, float* part, hipStream_t s) {
+  F8Args g{};
+  g.a = static_cast<const uint8_t*>(a8);
+  g.a_bytes = (uint32_t)(M * K);
+  g.as = as;
+  g.as_row = (int)as_row;
+  g.as_kb = (int)as_kb;
+  g.w = static_cast<const uint8_t*>(w);
+  g.w_bytes = (uint32_t)(N * K);
+  g.ws = ws;
+  g.K = (int)K;
+  g.KB = (int)((K + 127) / 128);
+  g.N = (int)N;
+  g.nblk = (int)((N + 127) / 128);
+  g.M = (int)M;
+  g.out = y;
+  g.ldo = (int)ldy;
+  g.out_f32 = out_f32;
+  g.part = part;
+  g.kslice = p.kslice;
+  const int tiles = (int)((M + p.bm - 1) / p.bm);
+  int rc = launch_f8<F8_LINEAR>(p, g, tiles, s);
+  if (rc || p.ksplit == 1) return rc;
+  const int64_t total = M * N;
+  const int64_t blocks = (total + 255) / 256;
+  hipLaunchKernelGGL(f8_join_kernel, dim3((unsigned)(blocks > 4096 ? 4096 : blocks)), dim3(256), 0, s, part,
+                     p.ksplit, (int)M, (int)N, y, (int)ldy, out_f32);
+  return (int)hipGetLastError();
+}
+
+int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspace, hipStream_t s) {
+  char* base = static_cast<char*>(workspace);
+  const int64_t HB = (p.H + 127) / 128, IB = (p.I + 127) / 128;
+  int* hdr = reinterpret_cast<int*>(base + p.hdr_off);
+  int* perm = reinterpret_cast<int*>(base + p.perm_off);
+  uint8_t* x8 = reinterpret_cast<uint8_t*>(base + p.x8_off);
+  float* xs = reinterpret_cast<float*>(base + p.xs_off);
+  uint8_t* h8 = reinterpret_cast<uint8_t*>(base + p.h8_off);
+  float* hs = reinterpret_cast<float*>(base + p.hs_off);
+  float* h32 = reinterpret_cast<float*>(base + p.h32_off);
+  void* y = base + p.y_off;
+
+  PrepArgs pa{};
+  pa.ids = c.ids;
+  pa.pairs = (int)p.P;
+  pa.E = (int)p.E;
+  pa.first = (int)c.first;
+  pa.bm = p.gu.bm;
+  pa.hdr = hdr;
+  pa.perm = perm;
+  pa.q.x = c.x;
+  pa.q.rows = p.T;
+  pa.q.cols = (int)p.H;
+  pa.q.ldx = p.H;
+  pa.q.bf16 = 1;
+  pa.q.q = x8;
+  pa.q.s = xs;
+  pa.q.s_row = 1;
+  pa.q.s_kb = p.T;
+  hipLaunchKernelGGL(experts_prep_kernel, dim3(1 + quant_grid(p.T * HB, kPrepThreads / 16)), dim3(kPrepThreads), 0,
+                     s, pa);
+  int rc = (int)hipGetLastError();
+  if (rc) return rc;
+
+  F8Args g{};
+  g.a = x8;
+  g.a_bytes = (uint32_t)(p.T * p.H);
+  g.as = xs;
+  g.as_row = 1;
+  g.as_kb = (int)p.T;
+  g.w = static_cast<const uint8_t*>(c.w_gate_up);
+  g.w_stride = (size_t)(2 * p.I * p.H);
+  g.w_bytes = (uint32_t)(2 * p.I * p.H);
+  g.ws = c.s_gate_up;
+  g.ws_stride = (size_t)(2 * IB * HB);
+  g.K = (int)p.H;
+  g.KB = (int)HB;
+  g.N = (int)p.I;
+  g.nblk = (int)IB;
+  g.hdr = hdr;
+  g.perm = perm;
+  g.topk = (int)p.topk;
+  g.ldo = (int)p.I;
+  g.kslice = (int)HB;
+  const bool stream = p.gu.kind == F8_KIND_STREAM;
+  g.out = stream ? static_cast<void*>(h32) : h8;
+  g.out_f32 = stream;
+  g.hs = hs;
+  g.hs_ld = (int)p.P;
+  if ((rc = launch_f8<F8_GATE_UP>(p.gu, g, (int)p.max_tiles, s))) return rc;
+  if (stream && (rc = launch_quant_fp8(h32, 0, 1, p.P, p.I, p.I, 1, h8, hs, 1, p.P, s))) return rc;
+
+  F8Args d{};
+  d.a = h8;
+  d.a_bytes = (uint32_t)(p.P * p.I);
+  d.as = hs;
+  d.as_row = 1;
+  d.as_kb = (int)p.P;
+  d.w = static_cast<const uint8_t*>(c.w_down);
+  d.w_stride = (size_t)(p.H * p.I);
+  d.w_bytes = (uint32_t)(p.H * p.I);
+  d.ws = c.s_down;
+  d.ws_stride = (size_t)(HB * IB);
+  d.K = (int)p.I;
+  d.KB = (int)IB;
+  d.N = (int)p.H;
+  d.nblk = (int)HB;
+  d.hdr = hdr;
+  d.perm = perm;
+  d.topk = (int)p.topk;
+  d.out = y;
+  d.ldo = (int)p.H;
+  d.out_f32 = p.y_f32;
+  d.kslice = (int)IB;
+  if ((rc = launch_f8<F8_DOWN>(p.dn, d, (int)p.max_tiles, s))) return rc;
+
+  CombineArgs ca{};
+  ca.y = y;
+  ca.y_f32 = p.y_f32;
+  ca.ids = c.ids;
+  ca.weights = c.weights;
+  ca.out = c.out;
+  ca.T = (int)p.T;
+  ca.H = (int)p.H;
+  ca.E = (int)p.E;
+  ca.first = (int)c.first;
+  ca.topk = (int)p.topk;
+  ca.out_f32 = c.out_f32;
+  const int64_t n = (p.T * (p.H / 8) + 255) / 256;
+  hipLaunchKernelGGL(experts_combine_kernel, dim3((unsigned)(n > 16384 ? 16384 : n)), dim3(256), 0, s, ca);
+  return (int)hipGetLastError();
+}
+
+}  // namespace smlp

@@ -4,7 +4,13 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "smlp.h"
+
 namespace smlp {
+
+// Record a status and its detail (shared_mlp_last_error) and return the status (api.cpp);
+// SMLP_OK clears the detail.
+int set_status(int status, const char* detail);
 
 // One weight-streaming (small-M) stage: out-features in blocks of 16, K split into
 // `ksplit` slices over workgroups and into `waves` slices inside a workgroup.
@@ -129,5 +135,52 @@ int launch_rms_rescale(const float* in, uint16_t* out, int64_t M, int64_t H, hip
 // bf16 -> fp16 copy of a rows x cols weight matrix (source row stride ld_src) into a dense
 // destination (aux.hip).
 int launch_bf16_to_f16(const void* src, int64_t ld_src, int64_t rows, int64_t cols, void* dst, hipStream_t s);
+
+// Routing to experts (route.hip); arguments validated by the caller.
+int launch_route(const void* logits, int bf16, int64_t T, int64_t E, int64_t ldl, const float* bias,
+                 const smlp_route& r, int32_t* ids, float* weights, hipStream_t s);
+
+// One 8-bit block-scaled product (fp8.hip).
+enum { F8_KIND_STREAM = 0, F8_KIND_TILE = 1 };
+struct F8Plan {
+  int kind;
+  int bm;                     // activation rows per tile
+  int nt, mt, waves, stages;  // streaming: 16-row weight and activation tiles, waves, ring stages
+  int bn;                     // tiled: weight rows per workgroup
+  int exact;                  // tiled: products through bf16 (fp32 results)
+  int ksplit, kslice;         // tiled projection: K slices over workgroups, 128-element blocks per slice
+};
+
+// Rows (parts x rows, row stride ldx elements) to e4m3 with one scale per row (block_rows 1;
+// scale of row r, group b at scales[r * s_row + b * s_kb]) or per block of 128 rows of a part
+// (dense [parts, row blocks, column blocks]) and 128 columns.
+int launch_quant_fp8(const void* x, int bf16, int64_t parts, int64_t rows, int64_t cols, int64_t ldx,
+                     int block_rows, void* q, float* scales, int64_t s_row, int64_t s_kb, hipStream_t s);
+int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t as_row, int64_t as_kb,
+                      const void* w, const float* ws, void* y, int64_t M, int64_t K, int64_t N, int64_t ldy,
+                      int out_f32, float* part, hipStream_t s);
+
+// The routed experts: sort, gate_up, (requantisation of h,) down, weighted sum (fp8.hip).
+struct ExpertsPlan {
+  int64_t T, H, I, E, topk;
+  int64_t P;            // pairs = T * topk
+  int64_t max_tiles;    // row tiles that any routing can need
+  F8Plan gu, dn;
+  int y_f32;            // rows of y held in fp32 (1) or bf16 (0)
+  size_t hdr_off, perm_off, x8_off, xs_off, h8_off, hs_off, h32_off, y_off, workspace_bytes;
+};
+struct ExpertsCall {
+  const void* x;
+  const int32_t* ids;
+  const float* weights;
+  const void* w_gate_up;
+  const float* s_gate_up;
+  const void* w_down;
+  const float* s_down;
+  void* out;
+  int64_t first;
+  int out_f32;
+};
+int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspace, hipStream_t s);
 
 }  // namespace smlp
