@@ -261,7 +261,7 @@ int shared_mlp_route(const void* logits, int dtype, int64_t T, int64_t E, int64_
 /*
  * The 8-bit form of a tensor: e4m3 values (OCP, largest finite value 448) with one fp32
  * scale per group, the value being q * scale.  With a = max(max|x| over the group, 1e-30):
- *   scale = a / 448,   q = e4m3_rne(x * (448 / a))        (each operation rounded to fp32)
+ *   scale = a / 448,   q = e4m3_rne(x * (448 * (1 / a)))  (each operation rounded to fp32)
  * A NaN stays a NaN; an infinity makes every product with its group a NaN.
  *   x       parts * rows rows of cols elements, row stride ldx; dtype SMLP_BF16 or
  *           SMLP_FP32; 16-byte aligned, ldx * element size a multiple of 16

@@ -453,7 +453,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
       float mx = kAmaxMin;
 #pragma unroll
       for (int v = 0; v < WN; ++v) mx = fmaxf(mx, red[v * BM + r]);
-      const float inv = kE4M3Max / mx;
+      const float inv = kE4M3Max * (1.0f / mx);
       if (r >= count) continue;
       if (wn == 0 && lg == 0) g.hs[(size_t)blk * g.hs_ld + start + r] = mx / kE4M3Max;
 #pragma unroll
@@ -547,7 +547,7 @@ __device__ __forceinline__ void quant_group(const QuantArgs& a, int64_t group, i
 #pragma unroll
   for (int d = 8; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
   if (!in) return;
-  const float inv = kE4M3Max / mx;
+  const float inv = kE4M3Max * (1.0f / mx);
   *reinterpret_cast<u32x2*>(a.q + (size_t)row * a.cols + c) =
       u32x2{pack_fp8x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
             pack_fp8x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
@@ -588,7 +588,7 @@ __global__ __launch_bounds__(256) void quant_blocks_kernel(QuantArgs a, int rows
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mx;
   __syncthreads();
   mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const float inv = kE4M3Max / mx;
+  const float inv = kE4M3Max * (1.0f / mx);
   for (int r = rr; r < nr; r += 16) {
     if (c >= a.cols) break;
     float v[8];

@@ -1,8 +1,8 @@
 """fp64 oracle of the routed half of the layer: routing to experts, the 8-bit block-scaled
 product and the routed experts' SwiGLU (numpy; shares no code with the library).
 
-The 8-bit form follows the format's definition: the scale a / 448, the reciprocal 448 / a
-and the scaled value are fp32 numbers, and the stored value is the nearest e4m3 value, ties
+The 8-bit form follows the format's definition: the scale a / 448, the factor
+448 (1 / a) and the scaled value are fp32 numbers, and the stored value is the nearest e4m3 value, ties
 to even.  Everything after that is fp64.
 """
 from __future__ import annotations
@@ -39,7 +39,7 @@ def quantize(x: np.ndarray, block_rows: int = 1):
             c = slice(b * BLOCK, (b + 1) * BLOCK)
             a = np.maximum(np.abs(x[r, c]).max(), np.float32(TINY))
             s[i, b] = a / np.float32(TOP)
-            q[r, c] = e4m3_round(x[r, c] * (np.float32(TOP) / a))
+            q[r, c] = e4m3_round(x[r, c] * (np.float32(TOP) * (np.float32(1.0) / a)))
     return q, s
 
 
