@@ -11,6 +11,7 @@ HIP runtime torch already loaded (one runtime per process).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -459,32 +460,54 @@ def shared_mlp_forward_rank(x, w_gate_up, w_down, out, tp: int, rank: int, works
 
 
 # The routed half of the layer (include/smlp.h): routing, the 8-bit block-scaled product, the
-# routed experts.
+# routed experts.  Decode calls take a few microseconds on the GPU, so the marshalling here is
+# kept short: sizes and options that repeat are looked up, never tensors.
 
 FP8 = torch.float8_e4m3fn
 ROUTE_SCORES = {"sigmoid": 0, "softmax": 1}
 
 
-def _typed(name, t, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+def _want(name, t, dtype, shape):
+    """t's address, after checks of type, shape, place and layout."""
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous GPU tensor")
+    return t.data_ptr()
 
 
-def _same_device(first, *others):
+def _want_rows(name, t, rows, cols):
+    """Address and row stride of a matrix whose rows are contiguous."""
+    if t.shape != (rows, cols) or not t.is_cuda:
+        raise ValueError(f"{name} must be a [{rows}, {cols}] GPU tensor, not {tuple(t.shape)} on {t.device}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+def _same_device(index, *others):
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on cuda:{index} and {t.device}")
+
+
+def _queue(stream, index):
+    """Raw handle of `stream`, or of the current stream of GPU `index`."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _blocks128(n: int) -> int:
     return (n + 127) // 128
 
 
-def _out2d(name, t, rows, cols):
-    """Row stride of an output whose rows are contiguous."""
-    if tuple(t.shape) != (rows, cols) or not t.is_cuda or (cols > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a [{rows}, {cols}] GPU tensor with unit column stride")
-    return t.stride(0) if rows > 1 else cols
+@functools.lru_cache(maxsize=256)
+def _route_options(score, groups, top_groups, group_top, topk, renormalize, scale):
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score {score!r} is not one of {sorted(ROUTE_SCORES)}")
+    return _Route(ROUTE_SCORES[score], int(groups), int(groups if top_groups is None else top_groups), int(group_top),
+                  int(topk), int(bool(renormalize)), float(scale))
 
 
 def shared_mlp_route(logits, ids, weights, score="sigmoid", bias=None, groups=1, top_groups=None, group_top=1,
@@ -493,25 +516,24 @@ def shared_mlp_route(logits, ids, weights, score="sigmoid", bias=None, groups=1,
     ids [T, topk] int32 and weights [T, topk] fp32 are written."""
     T, E = logits.shape
     topk = ids.shape[1]
-    ldl = _out2d("logits", logits, T, E)
-    _typed("ids", ids, torch.int32, (T, topk))
-    _typed("weights", weights, torch.float32, (T, topk))
-    if bias is not None:
-        _typed("bias", bias, torch.float32, (E,))
-    _same_device(logits, ids, weights, bias)
-    if score not in ROUTE_SCORES:
-        raise ValueError(f"score {score!r} is not one of {sorted(ROUTE_SCORES)}")
-    r = _Route(ROUTE_SCORES[score], int(groups), int(groups if top_groups is None else top_groups), int(group_top),
-               topk, int(bool(renormalize)), float(scale))
-    _check(lib().shared_mlp_route(logits.data_ptr(), _dtype_code(logits), T, E, ldl, _ptr(bias), ctypes.byref(r),
-                                  _ptr(ids), _ptr(weights), _stream(stream, logits.device)))
+    src, ldl = _want_rows("logits", logits, T, E)
+    r = _route_options(score, groups, top_groups, group_top, topk, renormalize, scale)
+    dev = logits.get_device()
+    _same_device(dev, ids, weights, bias)
+    rc = lib().shared_mlp_route(src, _dtype_code(logits), T, E, ldl,
+                                None if bias is None else _want("bias", bias, torch.float32, (E,)), r,
+                                _want("ids", ids, torch.int32, (T, topk)),
+                                _want("weights", weights, torch.float32, (T, topk)), _queue(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def route(logits, topk: int, score="sigmoid", bias=None, groups=1, top_groups=None, group_top=1, renormalize=True,
           scale=1.0, stream=None):
     """Allocating form of shared_mlp_route; returns ids, weights."""
-    ids = torch.empty(logits.shape[0], topk, dtype=torch.int32, device=logits.device)
-    weights = torch.empty(logits.shape[0], topk, dtype=torch.float32, device=logits.device)
+    T, dev = logits.shape[0], logits.device
+    ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
     shared_mlp_route(logits, ids, weights, score, bias, groups, top_groups, group_top, renormalize, scale, stream)
     return ids, weights
 
@@ -521,16 +543,17 @@ def shared_mlp_quant_fp8(x, q, scales, block_rows=1, stream=None):
     parts, rows, cols = x.shape if x.dim() == 3 else (1, *x.shape)
     if not x.is_cuda or x.stride(-1) != 1 or (x.dim() == 3 and parts > 1 and x.stride(0) != rows * x.stride(1)):
         raise ValueError("x must be a GPU tensor of equally spaced rows with unit column stride")
-    _typed("q", q, FP8, x.shape)
     lead = (parts,) if x.dim() == 3 else ()
-    _typed("scales", scales, torch.float32,
-           (*lead, rows if block_rows == 1 else _blocks128(rows), _blocks128(cols)))
-    _same_device(x, q, scales)
+    qp = _want("q", q, FP8, x.shape)
+    sp = _want("scales", scales, torch.float32,
+               (*lead, rows if block_rows == 1 else _blocks128(rows), _blocks128(cols)))
+    dev = x.get_device()
+    _same_device(dev, q, scales)
     ldx = x.stride(-2) if parts * rows > 1 else cols
     if rows == 0:
         return
-    _check(lib().shared_mlp_quant_fp8(x.data_ptr(), _dtype_code(x), parts, rows, cols, ldx, int(block_rows), _ptr(q),
-                                      _ptr(scales), _stream(stream, x.device)))
+    _check(lib().shared_mlp_quant_fp8(x.data_ptr(), _dtype_code(x), parts, rows, cols, ldx, int(block_rows), qp, sp,
+                                      _queue(stream, dev)))
 
 
 def quantize_fp8(x, block_rows=1, stream=None):
@@ -542,6 +565,7 @@ def quantize_fp8(x, block_rows=1, stream=None):
     return q, scales
 
 
+@functools.lru_cache(maxsize=1024)
 def shared_mlp_linear_fp8_workspace_bytes(M: int, K: int, N: int, x_fp8: bool) -> int:
     b = _sz()
     _check(lib().shared_mlp_linear_fp8_workspace_bytes(M, K, N, int(bool(x_fp8)), ctypes.byref(b)))
@@ -553,30 +577,35 @@ def shared_mlp_linear_fp8(x, w, w_scales, y, x_scales=None, workspace=None, stre
     x_scales [M, ceil(K / 128)]; y bf16 or fp32 [M, N], unit column stride."""
     M, K = x.shape
     N = w.shape[0]
-    _typed("x", x, torch.bfloat16 if x_scales is None else FP8, (M, K))
-    _typed("w", w, FP8, (N, K))
-    _typed("w_scales", w_scales, torch.float32, (_blocks128(N), _blocks128(K)))
-    if x_scales is not None:
-        _typed("x_scales", x_scales, torch.float32, (M, _blocks128(K)))
-    ldy = _out2d("y", y, M, N)
-    if y.dtype not in (torch.bfloat16, torch.float32):
+    KB = (K + 127) // 128
+    quantized = x_scales is not None
+    out_fp32 = y.dtype is torch.float32
+    if not out_fp32 and y.dtype is not torch.bfloat16:
         raise TypeError(f"y dtype {y.dtype} is neither bfloat16 nor float32")
-    _same_device(x, x_scales, w, w_scales, y, workspace)
+    yp, ldy = _want_rows("y", y, M, N)
+    xp = _want("x", x, FP8 if quantized else torch.bfloat16, (M, K))
+    wp = _want("w", w, FP8, (N, K))
+    wsp = _want("w_scales", w_scales, torch.float32, ((N + 127) // 128, KB))
+    xsp = _want("x_scales", x_scales, torch.float32, (M, KB)) if quantized else None
+    dev = x.get_device()
     if workspace is None:
-        need = shared_mlp_linear_fp8_workspace_bytes(M, K, N, x_scales is not None)
+        need = shared_mlp_linear_fp8_workspace_bytes(M, K, N, quantized)
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    _check(lib().shared_mlp_linear_fp8(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), y.data_ptr(), M, K, N, ldy,
-                                       int(y.dtype == torch.float32), _ptr(workspace), _ws_bytes(workspace),
-                                       _stream(stream, x.device)))
+    _same_device(dev, x_scales, w, w_scales, y, workspace)
+    rc = lib().shared_mlp_linear_fp8(xp, xsp, wp, wsp, yp, M, K, N, ldy, out_fp32, _ptr(workspace),
+                                     _ws_bytes(workspace), _queue(stream, dev))
+    if rc:
+        _check(rc)
     return y
 
 
 def linear_fp8(x, w, w_scales, x_scales=None, out_fp32=False, workspace=None, stream=None):
     """Allocating form of shared_mlp_linear_fp8."""
-    y = torch.empty(x.shape[0], w.shape[0], dtype=torch.float32 if out_fp32 else torch.bfloat16, device=x.device)
+    y = torch.empty((x.shape[0], w.shape[0]), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=x.device)
     return shared_mlp_linear_fp8(x, w, w_scales, y, x_scales, workspace, stream)
 
 
+@functools.lru_cache(maxsize=1024)
 def shared_mlp_experts_fp8_workspace_bytes(T: int, H: int, I: int, E: int, topk: int, partial_fp32=False) -> int:
     b = _sz()
     _check(lib().shared_mlp_experts_fp8_workspace_bytes(T, H, I, E, topk, int(bool(partial_fp32)), ctypes.byref(b)))
@@ -590,25 +619,23 @@ def shared_mlp_experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down
     T, H = x.shape
     E, _, I = w_down.shape
     topk = ids.shape[1]
-    _typed("x", x, torch.bfloat16, (T, H))
-    _typed("ids", ids, torch.int32, (T, topk))
-    _typed("weights", weights, torch.float32, (T, topk))
-    _typed("w_gate_up", w_gate_up, FP8, (E, 2 * I, H))
-    _typed("s_gate_up", s_gate_up, torch.float32, (E, 2 * _blocks128(I), _blocks128(H)))
-    _typed("w_down", w_down, FP8, (E, H, I))
-    _typed("s_down", s_down, torch.float32, (E, _blocks128(H), _blocks128(I)))
-    if out.dtype not in (torch.bfloat16, torch.float32):
+    HB, IB = (H + 127) // 128, (I + 127) // 128
+    partial = out.dtype is torch.float32
+    if not partial and out.dtype is not torch.bfloat16:
         raise TypeError(f"out dtype {out.dtype} is neither bfloat16 nor float32")
-    _typed("out", out, out.dtype, (T, H))
-    _same_device(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, out, workspace)
-    partial = out.dtype == torch.float32
+    dev = x.get_device()
+    args = (_want("x", x, torch.bfloat16, (T, H)), _want("ids", ids, torch.int32, (T, topk)),
+            _want("weights", weights, torch.float32, (T, topk)), _want("w_gate_up", w_gate_up, FP8, (E, 2 * I, H)),
+            _want("s_gate_up", s_gate_up, torch.float32, (E, 2 * IB, HB)), _want("w_down", w_down, FP8, (E, H, I)),
+            _want("s_down", s_down, torch.float32, (E, HB, IB)), _want("out", out, out.dtype, (T, H)))
     if workspace is None:
         need = shared_mlp_experts_fp8_workspace_bytes(T, H, I, E, topk, partial)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
-    _check(lib().shared_mlp_experts_fp8(_ptr(x), _ptr(ids), _ptr(weights), _ptr(w_gate_up), _ptr(s_gate_up),
-                                        _ptr(w_down), _ptr(s_down), _ptr(out), T, H, I, E, topk, int(first_expert),
-                                        int(partial), _ptr(workspace), _ws_bytes(workspace),
-                                        _stream(stream, x.device)))
+    _same_device(dev, ids, weights, w_gate_up, s_gate_up, w_down, s_down, out, workspace)
+    rc = lib().shared_mlp_experts_fp8(*args, T, H, I, E, topk, first_expert, partial, _ptr(workspace),
+                                      _ws_bytes(workspace), _queue(stream, dev))
+    if rc:
+        _check(rc)
     return out
 
 

@@ -68,6 +68,14 @@ __device__ __forceinline__ i32x8 lds_frag(const char* tile, int lane) {
   return v;
 }
 
+// One half (16 K elements per lane) of such a fragment into v[4 half .. 4 half + 3].
+__device__ __forceinline__ void lds_half(const char* tile, int lane, int half, i32x8& v) {
+  const int r = lane & 15, g = lane >> 4, sw = (r >> 1) & 7;
+  const u32x4 q = *reinterpret_cast<const u32x4*>(tile + r * 128 + (((g + 4 * half) ^ sw) * 16));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[4 * half + i] = (int)q[i];
+}
+
 // 4 bytes per lane from each lane's own address into 256 consecutive bytes of LDS.
 typedef const __attribute__((address_space(1))) void glb_void;
 __device__ __forceinline__ void glb_ld_lds4(const void* p, char* dst) {

@@ -79,6 +79,11 @@ __device__ __forceinline__ int f8_arow(const F8Args& g, int mode, int start, int
   return start + r;
 }
 
+// Byte offsets that make a buffer load return zeros: kNoRow in place of a row's offset,
+// kNoChunk added to one.  Buffers hold at most 2^31 - 16 bytes, so a real offset plus
+// kNoChunk, and kNoRow plus any, is out of range, and nothing wraps.
+constexpr uint32_t kNoRow = 0x80000000u, kNoChunk = 0x7ffffff0u;
+
 __device__ __forceinline__ void f8_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
@@ -157,12 +162,12 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
     for (int t = 0; t < NT; ++t) {
       const int f = f0 + 16 * (t % FT) + 8 * h + lr;
       const int row = t < FT ? f : g.N + f;
-      wo[t][h] = f < g.N ? (uint32_t)row * (uint32_t)K + ch[h] * 16 : g.w_bytes;
+      wo[t][h] = f < g.N ? (uint32_t)row * (uint32_t)K + ch[h] * 16 : kNoRow;
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const int r = 16 * t + 8 * h + lr;
-      ao[t][h] = r < count ? (uint32_t)f8_arow(g, MODE, start, r) * (uint32_t)K + ch[h] * 16 : g.a_bytes;
+      ao[t][h] = r < count ? (uint32_t)f8_arow(g, MODE, start, r) * (uint32_t)K + ch[h] * 16 : kNoRow;
     }
   }
   // Scale source of this lane: lanes 0 .. 16 MT - 1 the activation rows, lanes 32 and up
@@ -184,18 +189,15 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
     const int kb = i * WAVES + wave;
     const int k = kb * 128;
     char* sl = my + slot * SLOT;
+    const uint32_t ko[2] = {k + ch[0] * 16 < K ? (uint32_t)k : kNoChunk, k + ch[1] * 16 < K ? (uint32_t)k : kNoChunk};
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        buf_ld_lds_nt(wr, sl + t * 2048 + h * 1024,
-                      (k + ch[h] * 16 < K && wo[t][h] != g.w_bytes) ? wo[t][h] + k : g.w_bytes);
+      for (int h = 0; h < 2; ++h) buf_ld_lds_nt(wr, sl + t * 2048 + h * 1024, wo[t][h] + ko[h]);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        buf_ld_lds(ar, sl + (NT + t) * 2048 + h * 1024,
-                   (k + ch[h] * 16 < K && ao[t][h] != g.a_bytes) ? ao[t][h] + k : g.a_bytes);
+      for (int h = 0; h < 2; ++h) buf_ld_lds(ar, sl + (NT + t) * 2048 + h * 1024, ao[t][h] + ko[h]);
     glb_ld_lds4(sp + (size_t)min(kb, g.KB - 1) * sstep, sl + (NT + MT) * 2048);
   };
 
@@ -332,19 +334,18 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + (size_t)expert * g.w_stride, g.w_bytes);
   const __amdgpu_buffer_rsrc_t ar = make_rsrc(g.a, g.a_bytes);
 
-  // Block i of this wave: tile rows (i * W + wave) * 8 .. + 7.
+  // Block i of this wave: tile rows (i * W + wave) * 8 .. + 7; this lane's row and chunk.
+  static_assert(W % 2 == 0, "one chunk permutation for all blocks of a wave");
+  const int chk = (lane & 7) ^ ((4 * wave + (lr >> 1)) & 7);
   uint32_t aoff[AL], boff[BL];
-  int achk[AL], bchk[BL];
 #pragma unroll
   for (int i = 0; i < AL; ++i) {
     const int r = (i * W + wave) * 8 + lr;
-    achk[i] = (lane & 7) ^ ((r >> 1) & 7);
-    aoff[i] = r < count ? (uint32_t)f8_arow(g, MODE, start, r) * (uint32_t)K + achk[i] * 16 : g.a_bytes;
+    aoff[i] = r < count ? (uint32_t)f8_arow(g, MODE, start, r) * (uint32_t)K + chk * 16 : kNoRow;
   }
 #pragma unroll
   for (int i = 0; i < BL; ++i) {
     const int r = (i * W + wave) * 8 + lr;
-    bchk[i] = (lane & 7) ^ ((r >> 1) & 7);
     int f = f0 + r, row = f;
     if (GU) {
       // Each wave column's 16 * TN rows: its gate rows, then the matching up rows.
@@ -352,7 +353,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
       f = f0 + wc * 16 * FT + rr % (16 * FT);
       row = rr < 16 * FT ? f : g.N + f;
     }
-    boff[i] = f < g.N ? (uint32_t)row * (uint32_t)K + bchk[i] * 16 : g.w_bytes;
+    boff[i] = f < g.N ? (uint32_t)row * (uint32_t)K + chk * 16 : kNoRow;
   }
   // Scale source of this lane: lanes 0 .. RPW - 1 activation rows wave * RPW + lane, lanes
   // 32 and up the block of this wave's weight rows (odd lanes: of its up rows).
@@ -368,19 +369,26 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
     sstep = 1;
   }
 
-  auto issue = [&](int buf, int kb) {
+  // Load l of the LPS per wave and step: activation blocks, weight blocks, scales.  Data past
+  // the end of K arrives as zeros.  Steps are issued in order, so the scale pointer advances
+  // by one block each time, up to the last one.
+  auto issue_one = [&](int buf, int kb, int l) __attribute__((always_inline)) {
     char* st = lds + buf * STAGE;
-    const int k = kb * 128;
-#pragma unroll
-    for (int i = 0; i < AL; ++i)
-      buf_ld_lds(ar, st + (i * W + wave) * 1024,
-                 (aoff[i] != g.a_bytes && k + achk[i] * 16 < K) ? aoff[i] + k : g.a_bytes);
-#pragma unroll
-    for (int i = 0; i < BL; ++i)
-      buf_ld_lds(wr, st + A_BYTES + (i * W + wave) * 1024,
-                 (boff[i] != g.w_bytes && k + bchk[i] * 16 < K) ? boff[i] + k : g.w_bytes);
-    glb_ld_lds4(sp + (size_t)kb * sstep, st + A_BYTES + B_BYTES + wave * 256);
+    const uint32_t k = kb * 128 + chk * 16 < K ? (uint32_t)kb * 128u : kNoChunk;
+    if (l < AL) {
+      buf_ld_lds(ar, st + (l * W + wave) * 1024, aoff[l] + k);
+    } else if (l < AL + BL) {
+      buf_ld_lds(wr, st + A_BYTES + ((l - AL) * W + wave) * 1024, boff[l - AL] + k);
+    } else {
+      glb_ld_lds4(sp, st + A_BYTES + B_BYTES + wave * 256);
+      sp += kb + 1 < g.KB ? sstep : 0;
+    }
   };
+  auto issue = [&](int buf, int kb) {
+#pragma unroll
+    for (int l = 0; l < LPS; ++l) issue_one(buf, kb, l);
+  };
+  sp += (size_t)kb0 * sstep;
 
   f32x4 acc[TM][TN];
 #pragma unroll
@@ -388,41 +396,154 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  // Scale of row tile i in a stage: the fetching wave's region and place.
+  auto row_scale = [&](const char* sc, int i) __attribute__((always_inline)) {
+    const int r = (wm * TM + i) * 16 + ln;
+    return *reinterpret_cast<const float*>(sc + (r / RPW) * 256 + (r % RPW) * 4);
+  };
+
+  if constexpr (!EXACT) {
+    // Pinned schedule.  A step is TM x TN slots, row tile by row tile.  Slot m issues one
+    // matrix instruction and, while it runs, the four multiply-adds of slot m - 2, whose
+    // result has arrived by then; the fragments and scale of the next row tile are read
+    // during the present one.  The barrier that hands a stage back sits before the last row
+    // tile, whose operands every wave then holds in registers: that tile's matrix
+    // instructions cover the barrier, the reads of the next step's weights (each fragment
+    // right after its last use) and the first loads into the released stage; the remaining
+    // loads go out one per slot at the top of the next step.
+    constexpr int SLOTS = TM * TN;
+    static_assert(TM >= 2 && TM % 2 == 0 && SLOTS % 4 == 0, "fragment and result buffers alternate");
+    i32x8 wf[TN], af[2];
+    f32x4 p[4];
+    float sg[2] = {0.f, 0.f}, su[2] = {0.f, 0.f}, swg, swu;
+    p[2] = p[3] = f32x4{0.f, 0.f, 0.f, 0.f};  // the first step's slots 0 and 1 add nothing
+    auto madd = [&](int m) __attribute__((always_inline)) {
+      const int i = m / TN, j = m % TN;
+      const float sc = GU && j >= FT ? su[i & 1] : sg[i & 1];
 #pragma unroll
-  for (int st = 0; st < NS - 1; ++st)
-    if (st < nk) issue(st, kb0 + st);
-  for (int kt = 0; kt < nk; ++kt) {
-    f8_wait_steps<LPS, NS - 2>(min(NS - 2, nk - 1 - kt));
-    f8_barrier();
-    if (kt + NS - 1 < nk) issue((kt + NS - 1) % NS, kb0 + kt + NS - 1);
-    const char* st = lds + (kt % NS) * STAGE;
-    const char* sc = st + A_BYTES + B_BYTES;
-    const float swg = *reinterpret_cast<const float*>(sc + wave * 256 + 128);
-    const float swu = GU ? *reinterpret_cast<const float*>(sc + wave * 256 + 132) : swg;
-    auto frag = [&](const char* tile) {
-      if constexpr (EXACT) return widen(lds_frag(tile, lane));
-      else return lds_frag(tile, lane);
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[m & 3][e], sc, acc[i][j][e]);
     };
-    decltype(frag(st)) wf[TN];
-#pragma unroll
-    for (int j = 0; j < TN; ++j) wf[j] = frag(st + A_BYTES + (wn * TN + j) * 2048);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const auto af = frag(st + (wm * TM + i) * 2048);
-      const int r = (wm * TM + i) * 16 + ln;
-      const float s = *reinterpret_cast<const float*>(sc + (r / RPW) * 256 + (r % RPW) * 4);
-      const float sg = s * swg, su = s * swu;
+    auto read_af = [&](const char* st, int i, int half) __attribute__((always_inline)) {
+      lds_half(st + (wm * TM + i) * 2048, lane, half, af[i & 1]);
+    };
+    auto read_wf = [&](const char* st, int j) __attribute__((always_inline)) {
+      lds_half(st + A_BYTES + (wn * TN + j) * 2048, lane, 0, wf[j]);
+      lds_half(st + A_BYTES + (wn * TN + j) * 2048, lane, 1, wf[j]);
+    };
+    auto scales_of = [&](float s, int slot) __attribute__((always_inline)) {
+      sg[slot] = s * swg;
+      if constexpr (GU) su[slot] = s * swu;
+    };
+    constexpr int Q = (LPS + SLOTS - 1) / SLOTS;         // loads per slot
+    constexpr int HALF = Q * TN < LPS ? Q * TN : LPS;    // loads issued in the last row tile
+    // Slots of row tile i of a step (stage st); nst: the next step's stage (read in the last
+    // tile); loads l0 .. l1 - 1 of step lkb into stage lbuf go out Q per slot from the top.
+    auto row_tile = [&](int i, const char* st, const char* nst, int lbuf, int lkb, int l0, int l1)
+        __attribute__((always_inline)) {
+      const bool last = i == TM - 1;
+      const char* rst = last ? nst : st;
+      const int ri = last ? 0 : i + 1;
+      float s_next = 0.f, g_next = 0.f, u_next = 0.f;
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        f32x4 p;
-        if constexpr (EXACT) p = mfma_widened(wf[j], af);
-        else p = mfma_fp8(wf[j], af);
-        const float sj = j < FT ? sg : su;
+        const int m = i * TN + j;
+        p[m & 3] = mfma_fp8(wf[j], af[i & 1]);
+        madd((m + SLOTS - 2) % SLOTS);
+        if (last) read_wf(nst, j);
+        if (j == 0) {
+          s_next = row_scale(rst + A_BYTES + B_BYTES, ri);
+          read_af(rst, ri, 0);
+          if (TN == 1) read_af(rst, ri, 1);
+        }
+        if (j == 1) read_af(rst, ri, 1);
+        if (last && j == TN - 1) {
+          const float* w2 = reinterpret_cast<const float*>(nst + A_BYTES + B_BYTES + wave * 256 + 128);
+          g_next = w2[0];
+          if constexpr (GU) u_next = w2[1];
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sj, acc[i][j][e]);
+        for (int q = 0; q < Q; ++q)
+          if (l0 + j * Q + q < l1) issue_one(lbuf, lkb, l0 + j * Q + q);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if (last) {
+        swg = g_next;
+        swu = u_next;
+      }
+      scales_of(s_next, ri & 1);
+    };
+    // Every step of the ring is issued, those past the slice too (they are not used, and past
+    // K they read nothing), so the loop has no branches and its waits are constants.
+#pragma unroll
+    for (int st = 0; st < NS - 1; ++st) issue(st, kb0 + st);
+#pragma unroll
+    for (int l = 0; l < HALF; ++l) issue_one(NS - 1, kb0 + NS - 1, l);
+    wait_vmcnt<(NS - 2) * LPS + HALF>();
+    f8_barrier();
+    {
+      const char* st = lds;
+      const float* w2 = reinterpret_cast<const float*>(st + A_BYTES + B_BYTES + wave * 256 + 128);
+      swg = w2[0];
+      swu = GU ? w2[1] : 0.f;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) read_wf(st, j);
+      read_af(st, 0, 0);
+      read_af(st, 0, 1);
+      scales_of(row_scale(st + A_BYTES + B_BYTES, 0), 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_s_waitcnt(0xc07f);
+    for (int kt = 0; kt < nk; ++kt) {
+      const int cur = kt % NS, nxt = (kt + 1) % NS;
+      const char* st = lds + cur * STAGE;
+      const char* nst = lds + nxt * STAGE;
+      // The rest of step kt + NS - 1's loads (its first HALF went out in the last row tile of
+      // the step before).
+#pragma unroll
+      for (int i = 0; i < TM - 1; ++i)
+        row_tile(i, st, nst, (kt + NS - 1) % NS, kb0 + kt + NS - 1, HALF + i * TN * Q, LPS);
+      static_assert(HALF + (TM - 1) * TN * Q >= LPS, "a step's slots hold its loads");
+      // Every wave holds the last row tile's operands (lgkmcnt 0) and step kt + 1 has landed.
+      // (After the last step the reads below fetch fragments that are never used.)
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+      wait_vmcnt<(NS - 2) * LPS>();
+      f8_barrier();
+      row_tile(TM - 1, st, nst, cur, kb0 + kt + NS, 0, HALF);
+    }
+    wait_vmcnt<0>();
+    // The last two slots' multiply-adds; sg / su of the last row tile are still in place.
+    madd(SLOTS - 2);
+    madd(SLOTS - 1);
+    f8_barrier();
+  } else {
+#pragma unroll
+    for (int st = 0; st < NS - 1; ++st)
+      if (st < nk) issue(st, kb0 + st);
+    for (int kt = 0; kt < nk; ++kt) {
+      f8_wait_steps<LPS, NS - 2>(min(NS - 2, nk - 1 - kt));
+      f8_barrier();
+      if (kt + NS - 1 < nk) issue((kt + NS - 1) % NS, kb0 + kt + NS - 1);
+      const char* st = lds + (kt % NS) * STAGE;
+      const char* sc = st + A_BYTES + B_BYTES;
+      const float swg = *reinterpret_cast<const float*>(sc + wave * 256 + 128);
+      const float swu = GU ? *reinterpret_cast<const float*>(sc + wave * 256 + 132) : swg;
+      frag_bf16 wf[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) wf[j] = widen(lds_frag(st + A_BYTES + (wn * TN + j) * 2048, lane));
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const frag_bf16 af = widen(lds_frag(st + (wm * TM + i) * 2048, lane));
+        const float s = row_scale(sc, i);
+        const float sg = s * swg, su = s * swu;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const f32x4 p = mfma_widened(wf[j], af);
+          const float sj = j < FT ? sg : su;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sj, acc[i][j][e]);
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+    }
   }
 
   if constexpr (GU) {

@@ -37,21 +37,59 @@ __device__ __forceinline__ uint32_t choice_key(float c) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Maximum / sum over the 64 lanes, in every lane.
+// Data-parallel moves inside the wave (no LDS traffic): the lane `CTRL` names, or `old` where
+// there is none.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v, uint32_t old) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, 0xf, 0xf, false);
+}
+enum { SHR1 = 0x111, SHR2 = 0x112, SHR4 = 0x114, SHR8 = 0x118, BCAST15 = 0x142, BCAST31 = 0x143 };
+enum { XOR1 = 0xB1, XOR2 = 0x4E, HALF_MIRROR = 0x141, MIRROR = 0x140 };
+
+// Reductions over the 64 lanes: the last lane collects, the result is wave-uniform.
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
-  return v;
+  v = max(v, dpp<SHR1>(v, 0));
+  v = max(v, dpp<SHR2>(v, 0));
+  v = max(v, dpp<SHR4>(v, 0));
+  v = max(v, dpp<SHR8>(v, 0));
+  v = max(v, dpp<BCAST15>(v, 0));
+  v = max(v, dpp<BCAST31>(v, 0));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v, float old) {
+  return __uint_as_float(dpp<CTRL>(__float_as_uint(v), __float_as_uint(old)));
 }
 __device__ __forceinline__ float wave_max_f32(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
+  v = fmaxf(v, dpp_f<SHR1>(v, -INFINITY));
+  v = fmaxf(v, dpp_f<SHR2>(v, -INFINITY));
+  v = fmaxf(v, dpp_f<SHR4>(v, -INFINITY));
+  v = fmaxf(v, dpp_f<SHR8>(v, -INFINITY));
+  v = fmaxf(v, dpp_f<BCAST15>(v, -INFINITY));
+  v = fmaxf(v, dpp_f<BCAST31>(v, -INFINITY));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 __device__ __forceinline__ float wave_sum_f32(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  v += dpp_f<SHR1>(v, 0.f);
+  v += dpp_f<SHR2>(v, 0.f);
+  v += dpp_f<SHR4>(v, 0.f);
+  v += dpp_f<SHR8>(v, 0.f);
+  // The broadcasts add row 0 to row 1 and row 2 to row 3, then rows 0-1 to rows 2-3; only
+  // the last lane's sum is read, and it takes each row once.
+  v += dpp_f<BCAST15>(v, 0.f);
+  v += dpp_f<BCAST31>(v, 0.f);
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+// The two largest of (a1 >= a2) and (b1 >= b2).
+__device__ __forceinline__ void merge2(float& a1, float& a2, float b1, float b2) {
+  a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+  a1 = fmaxf(a1, b1);
+}
+
+__device__ __forceinline__ void wave_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
 }
 
 constexpr int kRouteWaves = 4;
@@ -60,116 +98,122 @@ constexpr int kRouteWaves = 4;
 // lowest lane with the largest key holds the lowest index.
 template <int VPT, bool BF>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
-  __shared__ float choice_lds[kRouteWaves][VPT * 64];
+  __shared__ float lds[kRouteWaves][VPT * 64];  // this wave's choices, then its scores
   const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = blockIdx.x * kRouteWaves + wave;
-  const bool live = t < a.T;
+  if (t >= a.T) return;  // waves are independent: no workgroup barrier below
   const int e0 = lane * VPT;
+  float* mine = lds[wave];
 
-  float score[VPT], choice[VPT];
-  uint32_t key[VPT];
-  float mx = -INFINITY;
+  float score[VPT], choice[VPT], bias[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) bias[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     float l = -INFINITY;
-    if (live && e0 + i < a.E) {
+    if (e0 + i < a.E) {
       const size_t at = (size_t)t * a.ldl + e0 + i;
       l = BF ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.logits)[at] << 16)
              : reinterpret_cast<const float*>(a.logits)[at];
     }
     score[i] = l;
-    mx = fmaxf(mx, l);
   }
   if (a.r.score == SMLP_SCORE_SIGMOID) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       score[i] = 1.0f / (1.0f + expf(-score[i]));
-      choice[i] = score[i];
+      choice[i] = a.bias ? score[i] + bias[i] : score[i];
     }
   } else {
+    float mx = score[0];
+#pragma unroll
+    for (int i = 1; i < VPT; ++i) mx = fmaxf(mx, score[i]);
     mx = wave_max_f32(mx);
     const float ref = mx == -INFINITY ? 0.0f : mx;  // a row of -inf: every term 0
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const float l = score[i];
-      const float p = expf(l - ref);
-      choice[i] = l;
-      score[i] = p;
-      sum += p;
+      choice[i] = score[i];
+      score[i] = expf(score[i] - ref);
+      sum += score[i];
     }
     sum = wave_sum_f32(sum);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       score[i] = sum == 0.0f ? 0.0f : score[i] / sum;
-      if (a.bias) choice[i] = score[i];
+      if (a.bias) choice[i] = score[i] + bias[i];
     }
   }
-  if (a.bias) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (e0 + i < a.E) choice[i] += a.bias[e0 + i];
-  }
+  uint32_t key[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) key[i] = e0 + i < a.E ? choice_key(choice[i]) : 0u;
 
   if (a.r.groups > 1) {
-    // Lane g sums group g's best choices (NaN counts as -inf); then the best groups.
+    // 2^s lanes per group scan its choices (NaN counts as -inf) and merge their two largest;
+    // then the best groups are taken one by one.
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) choice_lds[wave][e0 + i] = choice[i] == choice[i] ? choice[i] : -INFINITY;
-    __syncthreads();
-    uint32_t gkey = 0u;
-    if (lane < a.r.groups) {
-      float m1 = -INFINITY, m2 = -INFINITY;
-      for (int i = 0; i < a.per; ++i) {
-        const float c = choice_lds[wave][lane * a.per + i];
+    for (int i = 0; i < VPT; ++i) mine[e0 + i] = choice[i] == choice[i] ? choice[i] : -INFINITY;
+    wave_fence();
+    const int sh = __builtin_clz(a.r.groups - 1) - 26;  // 64 >> sh lanes hold all groups: 2^sh lanes each
+    const int grp = lane >> sh;
+    float m1 = -INFINITY, m2 = -INFINITY;
+    if (grp < a.r.groups)
+      for (int i = lane & ((1 << sh) - 1); i < a.per; i += 1 << sh) {
+        const float c = mine[grp * a.per + i];
         m2 = fmaxf(m2, fminf(m1, c));
         m1 = fmaxf(m1, c);
       }
-      gkey = choice_key(a.r.group_top == 2 ? m1 + m2 : m1);
-    }
+    // Within 2^k equal lanes, the mirrored lane of the next larger run stands for the other half.
+    if (sh > 0) merge2(m1, m2, dpp_f<XOR1>(m1, 0.f), dpp_f<XOR1>(m2, 0.f));
+    if (sh > 1) merge2(m1, m2, dpp_f<XOR2>(m1, 0.f), dpp_f<XOR2>(m2, 0.f));
+    if (sh > 2) merge2(m1, m2, dpp_f<HALF_MIRROR>(m1, 0.f), dpp_f<HALF_MIRROR>(m2, 0.f));
+    if (sh > 3) merge2(m1, m2, dpp_f<MIRROR>(m1, 0.f), dpp_f<MIRROR>(m2, 0.f));
+    if (sh > 4) merge2(m1, m2, __shfl_xor(m1, 16), __shfl_xor(m2, 16));
+    uint32_t gkey = grp < a.r.groups ? choice_key(a.r.group_top == 2 ? m1 + m2 : m1) : 0u;
     uint64_t stay = 0;
     for (int j = 0; j < a.r.top_groups; ++j) {
       const uint32_t best = wave_max_u32(gkey);
-      const int g = __ffsll((unsigned long long)__ballot(gkey == best)) - 1;
+      const int g = (__ffsll((unsigned long long)__ballot(gkey == best)) - 1) >> sh;
       stay |= 1ull << g;
-      if (lane == g) gkey = 0u;
+      if (grp == g) gkey = 0u;
     }
+    int of = e0 / a.per, left = a.per - (e0 - of * a.per);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (e0 + i >= a.E || !((stay >> ((e0 + i) / a.per)) & 1)) key[i] = 0u;
+    for (int i = 0; i < VPT; ++i) {
+      if (!((stay >> (of & 63)) & 1)) key[i] = 0u;
+      if (--left == 0) {
+        ++of;
+        left = a.per;
+      }
+    }
   }
+  wave_fence();
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) mine[e0 + i] = score[i];
 
   int my_id = 0;
-  float my_score = 0.0f;
   for (int j = 0; j < a.r.topk; ++j) {
     uint32_t best = key[0];
     int at = 0;
-    float s = score[0];
 #pragma unroll
     for (int i = 1; i < VPT; ++i)
       if (key[i] > best) {
         best = key[i];
         at = i;
-        s = score[i];
       }
     const uint32_t top = wave_max_u32(best);
     const int src = __ffsll((unsigned long long)__ballot(best == top)) - 1;
-    const int id = __shfl(e0 + at, src);
-    const float sc = __shfl(s, src);
-    if (lane == src) {
+    const int id = __builtin_amdgcn_readlane(e0 + at, src);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (i == at) key[i] = 0u;
-    }
-    if (lane == j) {
-      my_id = id;
-      my_score = sc;
-    }
+    for (int i = 0; i < VPT; ++i)
+      if (e0 + i == id) key[i] = 0u;
+    if (lane == j) my_id = id;
   }
-  const float sum = wave_sum_f32(my_score);  // lanes past topk hold 0
-  if (!live || lane >= a.r.topk) return;
+  wave_fence();
+  const float my_score = lane < a.r.topk ? mine[my_id] : 0.0f;
+  const float sum = wave_sum_f32(my_score);
+  if (lane >= a.r.topk) return;
   float w = my_score;
   if (a.r.renormalize) w = sum == 0.0f ? 0.0f : w / sum;
   const size_t at = (size_t)t * a.r.topk + lane;
