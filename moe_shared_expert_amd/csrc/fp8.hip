@@ -56,6 +56,11 @@ struct F8Args {
   int kslice;          // K blocks per slice
 };
 
+// Index of expert `id` among the E held from `first` on, or -1.
+__device__ __forceinline__ int local_expert(int id, int first, int E) {
+  return id >= first && id - first < E ? id - first : -1;
+}
+
 // Tile list of the experts' products: hdr[0] = tiles, then (expert, first sorted position,
 // rows) of each.
 __device__ __forceinline__ bool f8_tile(const F8Args& g, int mode, int bm, int tile, int& expert, int& start,
@@ -126,26 +131,63 @@ __device__ __forceinline__ void f8_store4(const F8Args& g, size_t row, int n, f3
   }
 }
 
+// Eight elements at p (16-byte aligned).
+__device__ __forceinline__ void load8(const void* x, size_t at, int bf16, float (&v)[8]) {
+  if (bf16) {
+    const u32x4 u = ld16(reinterpret_cast<const uint16_t*>(x) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf_lo(u[i]);
+      v[2 * i + 1] = bf_hi(u[i]);
+    }
+  } else {
+    const float* p = reinterpret_cast<const float*>(x) + at;
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  }
+}
+
+// Activation tiles of the streaming kernels come in AH blocks of 8 rows.  One block serves
+// up to 8 rows (lanes 8-15 of a fragment read it again): a product's column depends on its
+// own activation row only, so columns without a row may hold anything and are not stored.
+__device__ __forceinline__ i32x8 act_frag(const char* tile, int row, int lg) {
+  const int sw = (row >> 1) & 7;
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(tile + row * 128 + ((lg ^ sw) * 16));
+  const u32x4 hi = *reinterpret_cast<const u32x4*>(tile + row * 128 + (((lg + 4) ^ sw) * 16));
+  i32x8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = (int)lo[i];
+    v[4 + i] = (int)hi[i];
+  }
+  return v;
+}
+
 // Weight streaming (few rows per tile).  A workgroup owns NT tiles of 16 weight rows
-// (gate_up: NT / 2 tiles of gate rows and the matching up rows) and one tile of 16 * MT
+// (gate_up: NT / 2 tiles of gate rows and the matching up rows) and one tile of 8 * AH
 // activation rows; its waves take the K blocks in turn, each through a ring of its own, and
 // their sums are added in wave order.
-template <int NT, int MT, int WAVES, int STAGES, int MODE>
+template <int NT, int AH, int WAVES, int STAGES, int MODE>
 __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
   constexpr bool GU = MODE == F8_GATE_UP;
   constexpr int FT = GU ? NT / 2 : NT;  // feature tiles
-  constexpr int SLOT = (NT + MT) * 2048 + 256;
-  constexpr int LPS = 2 * (NT + MT) + 1;
+  constexpr int AR = 8 * AH, MT = (AH + 1) / 2;
+  constexpr int SLOT = NT * 2048 + AH * 1024 + 256;
+  constexpr int LPS = 2 * NT + AH + 1;
   constexpr int RING = WAVES * STAGES * SLOT;
   constexpr int RED = WAVES * NT * MT * 64 * 16;
-  static_assert(LPS * (STAGES - 1) < 64, "loads in flight");
+  static_assert(LPS * (STAGES - 1) < 64 && AR <= 32, "loads in flight");
   __shared__ __attribute__((aligned(1024))) char lds[RING > RED ? RING : RED];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ln = lane & 15, lg = lane >> 4, lr = lane >> 3;
   int expert, start, count;
-  if (!f8_tile(g, MODE, 16 * MT, blockIdx.y, expert, start, count)) return;
+  if (!f8_tile(g, MODE, AR, blockIdx.y, expert, start, count)) return;
   const int f0 = blockIdx.x * (16 * FT);
   const int K = g.K;
   const uint8_t* w = g.w + (size_t)expert * g.w_stride;
@@ -154,7 +196,7 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
   const __amdgpu_buffer_rsrc_t ar = make_rsrc(g.a, g.a_bytes);
 
   int ch[2];
-  uint32_t wo[NT][2], ao[MT][2];
+  uint32_t wo[NT][2], ao[AH];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     ch[h] = (lane & 7) ^ (((8 * h + lr) >> 1) & 7);
@@ -164,18 +206,18 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
       const int row = t < FT ? f : g.N + f;
       wo[t][h] = f < g.N ? (uint32_t)row * (uint32_t)K + ch[h] * 16 : kNoRow;
     }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int r = 16 * t + 8 * h + lr;
-      ao[t][h] = r < count ? (uint32_t)f8_arow(g, MODE, start, r) * (uint32_t)K + ch[h] * 16 : kNoRow;
-    }
   }
-  // Scale source of this lane: lanes 0 .. 16 MT - 1 the activation rows, lanes 32 and up
-  // the weight blocks (even lanes the gate or only one, odd lanes the up block).
+#pragma unroll
+  for (int h = 0; h < AH; ++h) {
+    const int r = 8 * h + lr;
+    ao[h] = r < count ? (uint32_t)f8_arow(g, MODE, start, r) * (uint32_t)K + ch[h & 1] * 16 : kNoRow;
+  }
+  // Scale source of this lane: lanes 0 .. AR - 1 the activation rows, lanes 32 and up the
+  // weight blocks (even lanes the gate or only one, odd lanes the up block).
   const float* sp;
   int sstep;
   if (lane < 32) {
-    sp = g.as + (size_t)f8_arow(g, MODE, start, min(lane & (16 * MT - 1), count - 1)) * g.as_row;
+    sp = g.as + (size_t)f8_arow(g, MODE, start, min(lane & (AR - 1), count - 1)) * g.as_row;
     sstep = g.as_kb;
   } else {
     const int blk = min(f0 / 128, g.nblk - 1) + (GU && (lane & 1) ? g.nblk : 0);
@@ -195,10 +237,8 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) buf_ld_lds_nt(wr, sl + t * 2048 + h * 1024, wo[t][h] + ko[h]);
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) buf_ld_lds(ar, sl + (NT + t) * 2048 + h * 1024, ao[t][h] + ko[h]);
-    glb_ld_lds4(sp + (size_t)min(kb, g.KB - 1) * sstep, sl + (NT + MT) * 2048);
+    for (int h = 0; h < AH; ++h) buf_ld_lds(ar, sl + NT * 2048 + h * 1024, ao[h] + ko[h & 1]);
+    glb_ld_lds4(sp + (size_t)min(kb, g.KB - 1) * sstep, sl + NT * 2048 + AH * 1024);
   };
 
   f32x4 acc[NT][MT];
@@ -208,22 +248,22 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
     for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
 #pragma unroll
-  for (int st = 0; st < STAGES - 1; ++st)
-    if (st < nst) issue(st, st);
+  for (int st = 0; st < STAGES - 1; ++st) issue(st, st);
   for (int i = 0; i < nst; ++i) {
     // The fragments of the slot about to be refilled were all read (and waited for) in the
-    // previous step.
-    if (i + STAGES - 1 < nst) issue((i + STAGES - 1) % STAGES, i + STAGES - 1);
-    f8_wait_steps<LPS, STAGES - 1>(min(STAGES - 1, nst - 1 - i));
+    // previous step.  Steps past K arrive as zeros without memory traffic.
+    issue((i + STAGES - 1) % STAGES, i + STAGES - 1);
+    wait_vmcnt<(STAGES - 1) * LPS>();
     asm volatile("" ::: "memory");
     const char* sl = my + (i % STAGES) * SLOT;
-    const float* sc = reinterpret_cast<const float*>(sl + (NT + MT) * 2048);
+    const float* sc = reinterpret_cast<const float*>(sl + NT * 2048 + AH * 1024);
     frag_bf16 af[MT];
     float sg[MT], su[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      af[m] = widen(lds_frag(sl + (NT + m) * 2048, lane));
-      const float s = sc[16 * m + ln];
+      const int row = (16 * m + ln) & (AR - 1);
+      af[m] = widen(act_frag(sl + NT * 2048, row, lg));
+      const float s = sc[row];
       sg[m] = s * sc[32];
       su[m] = GU ? s * sc[33] : sg[m];
     }
@@ -242,6 +282,7 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
   }
+  wait_vmcnt<0>();
 
   // Add the waves' sums in wave order; wave 0 finishes.
   if constexpr (WAVES > 1) {
@@ -278,6 +319,328 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
       f8_store4(g, row, n, v);
     }
   }
+}
+
+// Most 128-row blocks that a run of the short-K down kernel touches.
+constexpr int kDownBlocks = kDownRun / 8 + 2;
+
+// Down product of few rows per expert and a short K (KB <= KBMAX blocks).  A workgroup holds
+// its tile's activations (h in fp32, brought to the 8-bit form here) in LDS and streams a run
+// of `run` 16-row weight tiles; its waves take the tiles in turn, each wave with the whole K
+// and a ring of D blocks of 16 rows x 128 bytes that runs on from tile to tile.
+template <int AH, int KBMAX, int D>
+__global__ __launch_bounds__(256) void f8_down_kernel(F8Args g, const float* h, int run) {
+  constexpr int WAVES = 4, AR = 8 * AH, MT = (AH + 1) / 2;
+  constexpr int RING = WAVES * D * 2048, ACT = KBMAX * AR * 128;
+  __shared__ __attribute__((aligned(1024))) char lds[RING + ACT + KBMAX * (AR + kDownBlocks) * 4];
+  char* act = lds + RING;
+  float* sx = reinterpret_cast<float*>(lds + RING + ACT);
+  float* sw = sx + KBMAX * AR;  // this run's weight scales, from the block of its first row on
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ln = lane & 15, lg = lane >> 4, lr = lane >> 3;
+  int expert, start, count;
+  if (!f8_tile(g, F8_DOWN, AR, blockIdx.y, expert, start, count)) return;
+  const int K = g.K, KB = g.KB;
+  const int tiles = min(run, (g.N + 15) / 16 - (int)blockIdx.x * run);
+  const int n0 = blockIdx.x * run * 16;
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + (size_t)expert * g.w_stride, g.w_bytes);
+  const float* ws = g.ws + (size_t)expert * g.ws_stride;
+
+  const int mine = tiles > wave ? (tiles - wave + WAVES - 1) / WAVES : 0;
+  char* my = lds + wave * (D * 2048);
+  int ch[2];
+  uint32_t wo[2];  // this lane's two row offsets in the tile being issued
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    ch[q] = (lane & 7) ^ (((8 * q + lr) >> 1) & 7);
+    wo[q] = (uint32_t)(n0 + wave * 16 + 8 * q + lr) * (uint32_t)K + ch[q] * 16;
+  }
+  int ikb = 0, itile = 0;  // next block to issue
+  auto issue = [&](int slot) __attribute__((always_inline)) {
+    const int k = ikb * 128;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      buf_ld_lds_nt(wr, my + slot * 2048 + q * 1024,
+                    itile < mine && k + ch[q] * 16 < K ? wo[q] + (uint32_t)k : kNoRow);
+    if (++ikb == KB) {
+      ikb = 0;
+      ++itile;
+      wo[0] += (uint32_t)(WAVES * 16) * (uint32_t)K;
+      wo[1] += (uint32_t)(WAVES * 16) * (uint32_t)K;
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) issue(d);
+
+  // h rows -> e4m3 in LDS while the first weights travel: 16 lanes per row and group.
+  for (int q = threadIdx.x >> 4; q < count * KB; q += 16) {
+    const int r = q / KB, b = q - r * KB, l = threadIdx.x & 15, c = b * 128 + l * 8;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (c < K) load8(h, (size_t)(start + r) * K + c, 0, v);
+    float mx = kAmaxMin;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+    const float inv = kE4M3Max * (1.0f / mx);
+    *reinterpret_cast<u32x2*>(act + b * (AR * 128) + r * 128 + (((l >> 1) ^ ((r >> 1) & 7)) * 16) + (l & 1) * 8) =
+        u32x2{pack_fp8x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+              pack_fp8x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+    if (l == 0) sx[b * AR + r] = mx / kE4M3Max;
+  }
+  const int blk0 = n0 / 128, nb = (min(n0 + tiles * 16, g.N) + 127) / 128 - blk0;
+  for (int q = threadIdx.x; q < nb * KB; q += 256) sw[q] = ws[(size_t)blk0 * KB + q];
+  size_t row[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) row[m] = g.perm[start + min(16 * m + ln, count - 1)];
+  // LDS writes of every wave done; the ring's loads stay in flight.
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  f8_barrier();
+
+  f32x4 acc[MT];
+  int slot = 0;
+  for (int t = 0; t < mine; ++t) {
+    const int n = n0 + (wave + t * WAVES) * 16;
+    const float* swr = sw + (n / 128 - blk0) * KB;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int kb = 0; kb < KB; ++kb) {
+      issue(slot == 0 ? D - 1 : slot - 1);
+      wait_vmcnt<2 * (D - 1)>();
+      asm volatile("" ::: "memory");
+      const frag_bf16 wf = widen(lds_frag(my + slot * 2048, lane));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int r = (16 * m + ln) & (AR - 1);
+        const f32x4 p = mfma_widened(wf, widen(act_frag(act + kb * (AR * 128), r, lg)));
+        const float s = sx[kb * AR + r] * swr[kb];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][j] = fmaf(p[j], s, acc[m][j]);
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // this slot's reads are done
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+      slot = slot == D - 1 ? 0 : slot + 1;
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      if (16 * m + ln < count) f8_store4(g, row[m], n + 4 * lg, acc[m]);
+  }
+  wait_vmcnt<0>();
+}
+
+// ---- one token ----
+// A single token needs no sort and no sum over workgroups: gate_up works per pair on x
+// quantised in each workgroup, and down per 8 output rows over all pairs, so the whole call
+// is two launches.
+struct TokenArgs {
+  const uint16_t* x;     // [H] bf16
+  const int32_t* ids;    // [topk]
+  const float* weights;  // [topk]
+  const uint8_t* w;      // gate_up, or down, of expert e at w + e * w_stride
+  size_t w_stride;
+  uint32_t w_bytes;
+  const float* ws;
+  size_t ws_stride;
+  int H, I, HB, IB, E, first, topk;
+  float* h;              // [topk, I] fp32
+  void* out;
+  int out_f32;
+};
+
+// Eight values -> e4m3 with the scale of the 16 lanes that share a group.
+__device__ __forceinline__ u32x2 quant8(const float (&v)[8], float& scale) {
+  float mx = kAmaxMin;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+  const float inv = kE4M3Max * (1.0f / mx);
+  scale = mx / kE4M3Max;
+  return u32x2{pack_fp8x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+               pack_fp8x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+}
+
+// The same activation row in all 16 columns: block of 128 values at p.
+__device__ __forceinline__ frag_bf16 row_frag(const char* p, int lg) {
+  i32x8 v;
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(p + lg * 16), hi = *reinterpret_cast<const u32x4*>(p + 64 + lg * 16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = (int)lo[i];
+    v[4 + i] = (int)hi[i];
+  }
+  return widen(v);
+}
+
+// Workgroup (b, j): features 8 b .. 8 b + 7 of pair j.  One 16-row weight tile: 8 gate rows,
+// then the matching up rows; the four waves take the K blocks in turn.
+template <int STAGES>
+__global__ __launch_bounds__(256) void f8_token_gate_up_kernel(TokenArgs a) {
+  constexpr int WAVES = 4, RING = WAVES * STAGES * 2048;
+  __shared__ __attribute__((aligned(1024))) char lds[RING + kTokenBlocks * (128 + 12)];
+  char* x8 = lds + RING;
+  float* sx = reinterpret_cast<float*>(lds + RING + kTokenBlocks * 128);
+  float* sw = sx + kTokenBlocks;  // gate scales, then up scales
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lg = lane >> 4, lr = lane >> 3;
+  const int pair = blockIdx.y, f0 = blockIdx.x * 8, K = a.H, KB = a.HB;
+  const int expert = local_expert(a.ids[pair], a.first, a.E);
+  if (expert < 0) return;
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (size_t)expert * a.w_stride, a.w_bytes);
+  char* my = lds + wave * (STAGES * 2048);
+  int ch[2];
+  uint32_t wo[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    ch[q] = (lane & 7) ^ (((8 * q + lr) >> 1) & 7);
+    wo[q] = (uint32_t)(q * a.I + f0 + lr) * (uint32_t)K + ch[q] * 16;
+  }
+  const int nst = (KB + WAVES - 1) / WAVES;
+  auto issue = [&](int slot, int i) {
+    const int k = (i * WAVES + wave) * 128;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      buf_ld_lds_nt(wr, my + slot * 2048 + q * 1024, k + ch[q] * 16 < K ? wo[q] + (uint32_t)k : kNoRow);
+  };
+#pragma unroll
+  for (int st = 0; st < STAGES - 1; ++st) issue(st, st);
+  for (int b = threadIdx.x >> 4; b < KB; b += 16) {
+    const int l = threadIdx.x & 15, c = b * 128 + l * 8;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sc;
+    if (c < K) load8(a.x, c, 1, v);
+    *reinterpret_cast<u32x2*>(x8 + c) = quant8(v, sc);
+    if (l == 0) sx[b] = sc;
+  }
+  const float* ws = a.ws + (size_t)expert * a.ws_stride + (size_t)(f0 / 128) * KB;
+  for (int q = threadIdx.x; q < 2 * KB; q += 256)
+    sw[(q < KB ? 0 : kTokenBlocks - KB) + q] = ws[q < KB ? q : (size_t)a.IB * KB + q - KB];
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // LDS writes done; the ring's loads stay in flight
+  f8_barrier();
+
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < nst; ++i) {
+    issue((i + STAGES - 1) % STAGES, i + STAGES - 1);
+    wait_vmcnt<2 * (STAGES - 1)>();
+    asm volatile("" ::: "memory");
+    const int kb = min(i * WAVES + wave, KB - 1);  // past K the weights are zeros
+    const frag_bf16 wf = widen(lds_frag(my + (i % STAGES) * 2048, lane));
+    const f32x4 p = mfma_widened(wf, row_frag(x8 + kb * 128, lg));
+    const float s = sx[kb] * sw[(lg >> 1) * kTokenBlocks + kb];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = fmaf(p[j], s, acc[j]);
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+  }
+  wait_vmcnt<0>();
+  __syncthreads();
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+  red[wave * 64 + lane] = acc;
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int v = 1; v < WAVES; ++v) acc += red[v * 64 + lane];
+  f32x4 hv;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) hv[j] = silu_mul(acc[j], __shfl_xor(acc[j], 32));  // up rows sit 32 lanes on
+  if ((lane & 15) == 0 && lg < 2) *reinterpret_cast<f32x4*>(a.h + (size_t)pair * a.I + f0 + 4 * lg) = hv;
+}
+
+// Workgroup b: output rows 8 b .. 8 b + 7.  Wave w sums pairs w, w + 4, ... over the whole K
+// through a ring of D blocks of 8 rows x 128 bytes; the waves' sums are added in wave order.
+template <int D>
+__global__ __launch_bounds__(256) void f8_token_down_kernel(TokenArgs a) {
+  constexpr int WAVES = 4, RING = WAVES * D * 1024;
+  __shared__ __attribute__((aligned(1024))) char lds[RING + kTokenPairBlocks * (128 + 8)];
+  __shared__ int expert_of[SMLP_MAX_TOPK];
+  char* h8 = lds + RING;
+  float* sh = reinterpret_cast<float*>(lds + RING + kTokenPairBlocks * 128);
+  float* sw = sh + kTokenPairBlocks;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ln = lane & 15, lg = lane >> 4, lr = lane >> 3;
+  const int n0 = blockIdx.x * 8, K = a.I, KB = a.IB;
+  if ((int)threadIdx.x < a.topk) expert_of[threadIdx.x] = local_expert(a.ids[threadIdx.x], a.first, a.E);
+  __syncthreads();
+  char* my = lds + wave * (D * 1024);
+  const int ch = (lane & 7) ^ ((lr >> 1) & 7);
+  const uint32_t wo = (uint32_t)(n0 + lr) * (uint32_t)K + ch * 16;
+  // The local pairs of this wave, in order: next one at or after j.
+  auto next_pair = [&](int j) {
+    while (j < a.topk && __builtin_amdgcn_readfirstlane(expert_of[j]) < 0) j += WAVES;
+    return j;
+  };
+  auto rsrc_of = [&](int j) {
+    const int e = j < a.topk ? __builtin_amdgcn_readfirstlane(expert_of[j]) : 0;
+    return make_rsrc(a.w + (size_t)e * a.w_stride, j < a.topk ? a.w_bytes : 0u);
+  };
+  int ij = next_pair(wave), ikb = 0;
+  __amdgpu_buffer_rsrc_t wr = rsrc_of(ij);
+  auto issue = [&](int slot) __attribute__((always_inline)) {
+    const int k = ikb * 128;
+    buf_ld_lds_nt(wr, my + slot * 1024, k + ch * 16 < K ? wo + (uint32_t)k : kNoRow);
+    if (++ikb == KB) {
+      ikb = 0;
+      ij = next_pair(ij < a.topk ? ij + WAVES : ij);
+      wr = rsrc_of(ij);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) issue(d);
+  for (int q = threadIdx.x >> 4; q < a.topk * KB; q += 16) {
+    const int j = q / KB, b = q - j * KB, l = threadIdx.x & 15, c = b * 128 + l * 8;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sc;
+    if (c < K && expert_of[j] >= 0) load8(a.h, (size_t)j * K + c, 0, v);
+    *reinterpret_cast<u32x2*>(h8 + q * 128 + l * 8) = quant8(v, sc);
+    if (l == 0) {
+      sh[q] = sc;
+      sw[q] = expert_of[j] < 0 ? 0.f : a.ws[(size_t)expert_of[j] * a.ws_stride + (size_t)(n0 / 128) * KB + b];
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  f8_barrier();
+
+  f32x4 sum{0.f, 0.f, 0.f, 0.f};
+  int slot = 0;
+  for (int j = next_pair(wave); j < a.topk; j = next_pair(j + WAVES)) {
+    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+    for (int kb = 0; kb < KB; ++kb) {
+      issue(slot == 0 ? D - 1 : slot - 1);
+      wait_vmcnt<D - 1>();
+      asm volatile("" ::: "memory");
+      const frag_bf16 wf = widen(act_frag(my + slot * 1024, ln & 7, lg));
+      const int q = j * KB + kb;
+      const f32x4 p = mfma_widened(wf, row_frag(h8 + q * 128, lg));
+      const float s = sh[q] * sw[q];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(p[i], s, acc[i]);
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+      slot = slot == D - 1 ? 0 : slot + 1;
+    }
+    const float wt = a.weights[j];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = fmaf(wt, acc[i], sum[i]);
+  }
+  wait_vmcnt<0>();
+  __syncthreads();
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+  red[wave * 64 + lane] = sum;
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int v = 1; v < WAVES; ++v) sum += red[v * 64 + lane];
+  if (ln != 0 || lg >= 2) return;  // rows 8 .. 15 of the tile repeat rows 0 .. 7
+  const int n = n0 + 4 * lg;
+  if (a.out_f32) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + n) = sum;
+  else
+    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + n) =
+        u32x2{pack_bf2(sum[0], sum[1]), pack_bf2(sum[2], sum[3])};
 }
 
 // Workgroup -> (tile_m, tile_n): each XCD (workgroups are handed out round-robin over the 8)
@@ -634,26 +997,6 @@ struct QuantArgs {
   int64_t s_row, s_kb;
 };
 
-// Eight elements at p (16-byte aligned).
-__device__ __forceinline__ void load8(const void* x, size_t at, int bf16, float (&v)[8]) {
-  if (bf16) {
-    const u32x4 u = ld16(reinterpret_cast<const uint16_t*>(x) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf_lo(u[i]);
-      v[2 * i + 1] = bf_hi(u[i]);
-    }
-  } else {
-    const float* p = reinterpret_cast<const float*>(x) + at;
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
-    }
-  }
-}
-
 __device__ __forceinline__ void quant_group(const QuantArgs& a, int64_t group, int KB) {
   const int l = threadIdx.x & 15;
   const int64_t row = group / KB;
@@ -719,11 +1062,6 @@ __global__ __launch_bounds__(256) void quant_blocks_kernel(QuantArgs a, int rows
               pack_fp8x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
   }
   if (threadIdx.x == 0) a.s[(rb * KB) + b] = mx / kE4M3Max;
-}
-
-// Index of expert `id` among the E held from `first` on, or -1.
-__device__ __forceinline__ int local_expert(int id, int first, int E) {
-  return id >= first && id - first < E ? id - first : -1;
 }
 
 // First launch of the experts: workgroup 0 sorts the pairs (token, choice) by expert and
@@ -847,12 +1185,12 @@ int launch_f8(const F8Plan& p, const F8Args& a, int max_tiles, hipStream_t s) {
   if (p.kind == F8_KIND_STREAM) {
     const int per = (MODE == F8_GATE_UP ? 8 : 16) * p.nt;
     const dim3 grid((unsigned)((a.N + per - 1) / per), (unsigned)max_tiles);
-#define SMLP_F8(NT_, MT_, W_, S_)                                                                      \
-  if (p.nt == NT_ && p.mt == MT_ && p.waves == W_ && p.stages == S_) {                                 \
-    hipLaunchKernelGGL((f8_stream_kernel<NT_, MT_, W_, S_, MODE>), grid, dim3(W_ * 64), 0, s, a);      \
+#define SMLP_F8(NT_, AH_, W_, S_)                                                                      \
+  if (p.nt == NT_ && p.bm == 8 * AH_) {                                                                \
+    hipLaunchKernelGGL((f8_stream_kernel<NT_, AH_, W_, S_, MODE>), grid, dim3(W_ * 64), 0, s, a);      \
     return (int)hipGetLastError();                                                                     \
   }
-    SMLP_F8(2, 1, 4, 4) SMLP_F8(2, 2, 4, 4)
+    SMLP_F8(2, 1, 4, 3) SMLP_F8(2, 2, 4, 3) SMLP_F8(2, 4, 4, 4)
 #undef SMLP_F8
     return (int)hipErrorInvalidConfiguration;
   }
@@ -933,6 +1271,22 @@ int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t 
   return (int)hipGetLastError();
 }
 
+namespace {
+
+int launch_f8_down(const F8Plan& p, const F8Args& a, const float* h, int max_tiles, hipStream_t s) {
+  const dim3 grid((unsigned)(((a.N + 15) / 16 + p.run - 1) / p.run), (unsigned)max_tiles);
+#define SMLP_F8(AH_, KB_, D_)                                                                             \
+  if (p.bm == 8 * AH_ && a.KB <= KB_) {                                                                   \
+    hipLaunchKernelGGL((f8_down_kernel<AH_, KB_, D_>), grid, dim3(256), 0, s, a, h, p.run);               \
+    return (int)hipGetLastError();                                                                        \
+  }
+  SMLP_F8(1, 8, 6) SMLP_F8(2, 8, 6) SMLP_F8(4, 8, 6) SMLP_F8(1, 16, 6) SMLP_F8(2, 16, 5)
+#undef SMLP_F8
+  return (int)hipErrorInvalidConfiguration;
+}
+
+}  // namespace
+
 int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspace, hipStream_t s) {
   char* base = static_cast<char*>(workspace);
   const int64_t HB = (p.H + 127) / 128, IB = (p.I + 127) / 128;
@@ -945,6 +1299,37 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
   float* h32 = reinterpret_cast<float*>(base + p.h32_off);
   void* y = base + p.y_off;
 
+  if (p.token) {
+    TokenArgs t{};
+    t.x = static_cast<const uint16_t*>(c.x);
+    t.ids = c.ids;
+    t.weights = c.weights;
+    t.w = static_cast<const uint8_t*>(c.w_gate_up);
+    t.w_stride = (size_t)(2 * p.I * p.H);
+    t.w_bytes = (uint32_t)(2 * p.I * p.H);
+    t.ws = c.s_gate_up;
+    t.ws_stride = (size_t)(2 * IB * HB);
+    t.H = (int)p.H;
+    t.I = (int)p.I;
+    t.HB = (int)HB;
+    t.IB = (int)IB;
+    t.E = (int)p.E;
+    t.first = (int)c.first;
+    t.topk = (int)p.topk;
+    t.h = h32;
+    t.out = c.out;
+    t.out_f32 = c.out_f32;
+    hipLaunchKernelGGL((f8_token_gate_up_kernel<5>), dim3((unsigned)(p.I / 8), (unsigned)p.topk), dim3(256), 0, s, t);
+    int rc = (int)hipGetLastError();
+    if (rc) return rc;
+    t.w = static_cast<const uint8_t*>(c.w_down);
+    t.w_stride = (size_t)(p.H * p.I);
+    t.w_bytes = (uint32_t)(p.H * p.I);
+    t.ws = c.s_down;
+    t.ws_stride = (size_t)(HB * IB);
+    hipLaunchKernelGGL((f8_token_down_kernel<6>), dim3((unsigned)(p.H / 8)), dim3(256), 0, s, t);
+    return (int)hipGetLastError();
+  }
   PrepArgs pa{};
   pa.ids = c.ids;
   pa.pairs = (int)p.P;
@@ -993,7 +1378,8 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
   g.hs = hs;
   g.hs_ld = (int)p.P;
   if ((rc = launch_f8<F8_GATE_UP>(p.gu, g, (int)p.max_tiles, s))) return rc;
-  if (stream && (rc = launch_quant_fp8(h32, 0, 1, p.P, p.I, p.I, 1, h8, hs, 1, p.P, s))) return rc;
+  const bool short_k = p.dn.kind == F8_KIND_DOWN;
+  if (stream && !short_k && (rc = launch_quant_fp8(h32, 0, 1, p.P, p.I, p.I, 1, h8, hs, 1, p.P, s))) return rc;
 
   F8Args d{};
   d.a = h8;
@@ -1017,7 +1403,8 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
   d.ldo = (int)p.H;
   d.out_f32 = p.y_f32;
   d.kslice = (int)IB;
-  if ((rc = launch_f8<F8_DOWN>(p.dn, d, (int)p.max_tiles, s))) return rc;
+  rc = short_k ? launch_f8_down(p.dn, d, h32, (int)p.max_tiles, s) : launch_f8<F8_DOWN>(p.dn, d, (int)p.max_tiles, s);
+  if (rc) return rc;
 
   CombineArgs ca{};
   ca.y = y;

@@ -141,11 +141,12 @@ int launch_route(const void* logits, int bf16, int64_t T, int64_t E, int64_t ldl
                  const smlp_route& r, int32_t* ids, float* weights, hipStream_t s);
 
 // One 8-bit block-scaled product (fp8.hip).
-enum { F8_KIND_STREAM = 0, F8_KIND_TILE = 1 };
+enum { F8_KIND_STREAM = 0, F8_KIND_TILE = 1, F8_KIND_DOWN = 2 };
 struct F8Plan {
   int kind;
   int bm;                     // activation rows per tile
-  int nt, mt, waves, stages;  // streaming: 16-row weight and activation tiles, waves, ring stages
+  int nt;                     // streaming: 16-row weight tiles per workgroup
+  int run;                    // short-K down: 16-row weight tiles per workgroup
   int bn;                     // tiled: weight rows per workgroup
   int exact;                  // tiled: products through bf16 (fp32 results)
   int ksplit, kslice;         // tiled projection: K slices over workgroups, 128-element blocks per slice
@@ -160,12 +161,17 @@ int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t 
                       const void* w, const float* ws, void* y, int64_t M, int64_t K, int64_t N, int64_t ldy,
                       int out_f32, float* part, hipStream_t s);
 
+// Limits of the short-K down kernel (16-row weight tiles per workgroup) and of the kernels
+// for one token (blocks of 128 in H; blocks of 128 in I over all pairs).
+constexpr int kDownRun = 496, kTokenBlocks = 64, kTokenPairBlocks = 64;
+
 // The routed experts: sort, gate_up, (requantisation of h,) down, weighted sum (fp8.hip).
 struct ExpertsPlan {
   int64_t T, H, I, E, topk;
   int64_t P;            // pairs = T * topk
   int64_t max_tiles;    // row tiles that any routing can need
   F8Plan gu, dn;
+  int token;            // one token: two launches without a sort
   int y_f32;            // rows of y held in fp32 (1) or bf16 (0)
   size_t hdr_off, perm_off, x8_off, xs_off, h8_off, hs_off, h32_off, y_off, workspace_bytes;
 };

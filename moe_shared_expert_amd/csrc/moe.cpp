@@ -10,6 +10,7 @@
 
 namespace {
 
+constexpr int64_t kCUs = 256;  // compute units the grids are sized for
 constexpr int64_t kLimit = (int64_t)1 << 31;
 
 int fail(int status, const char* fmt, ...) {
@@ -50,14 +51,12 @@ size_t round_up(size_t v) { return (v + 255) / 256 * 256; }
 // a * b < 2^31 for non-negative a and b, without overflow.
 bool fits(int64_t a, int64_t b) { return a < kLimit && b < kLimit && a * b < kLimit; }
 
+// Streaming tiles of 8, 16 or 32 activation rows.
 smlp::F8Plan stream_plan(int64_t rows, int64_t KB) {
   smlp::F8Plan p{};
   p.kind = smlp::F8_KIND_STREAM;
   p.nt = 2;
-  p.mt = rows > 16 ? 2 : 1;
-  p.bm = 16 * p.mt;
-  p.waves = 4;
-  p.stages = 4;
+  p.bm = rows > 16 ? 32 : rows > 8 ? 16 : 8;
   p.ksplit = 1;
   p.kslice = (int)KB;
   return p;
@@ -134,11 +133,20 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
   if (rows <= 24) {
     p.gu = stream_plan(rows * 2, HB);
     p.dn = stream_plan(rows * 2, IB);
+    if (IB * p.dn.bm <= 256) {
+      // The whole K of a tile's activations fits LDS: about four workgroups per compute unit
+      // over the (tile, run of weight tiles) pairs, at least four weight tiles each.
+      p.dn.kind = smlp::F8_KIND_DOWN;
+      const int64_t ht = (H + 15) / 16, tiles = active ? p.P / p.dn.bm + active : 1;
+      const int64_t runs = (4 * kCUs + tiles - 1) / tiles, run = (ht + runs - 1) / runs;
+      p.dn.run = (int)(run < 4 ? 4 : run > smlp::kDownRun ? smlp::kDownRun : (run + 3) / 4 * 4);
+    }
   } else {
     const int bm = rows >= 192 ? 256 : 64;
     p.gu = tile_plan(bm, 256, HB, partial_fp32 != 0);
     p.dn = tile_plan(bm, 256, IB, partial_fp32 != 0);
   }
+  p.token = T == 1 && HB <= smlp::kTokenBlocks && topk * IB <= smlp::kTokenPairBlocks;
   const bool stream = p.gu.kind == smlp::F8_KIND_STREAM;
   p.y_f32 = stream || partial_fp32;
   // An expert with c rows needs ceil(c / bm) tiles.
