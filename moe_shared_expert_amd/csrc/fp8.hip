@@ -371,30 +371,53 @@ __global__ __launch_bounds__(256) void f8_down_kernel(F8Args g, const float* h, 
       wo[1] += (uint32_t)(WAVES * 16) * (uint32_t)K;
     }
   };
+  // h rows -> e4m3 in LDS, 16 lanes per row and group of 128.  Loads complete in order, so
+  // the first HP rounds of h (and the scales and places of the results) are loaded ahead of
+  // the ring's weights; more rounds only come with more than HP * 16 / KB rows.
+  constexpr int HP = 3;
+  const int l = threadIdx.x & 15;
+  float hv[HP][8];
+  auto load_h = [&](int q, float (&v)[8]) __attribute__((always_inline)) {
+    const int r = q / KB, c = (q - r * KB) * 128 + l * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    if (q < count * KB && c < K) load8(h, (size_t)(start + r) * K + c, 0, v);
+  };
+#pragma unroll
+  for (int i = 0; i < HP; ++i) load_h(i * 16 + (threadIdx.x >> 4), hv[i]);
+  const int blk0 = n0 / 128, nb = (min(n0 + tiles * 16, g.N) + 127) / 128 - blk0;
+  float swv = 0.f;
+  if ((int)threadIdx.x < nb * KB) swv = ws[(size_t)blk0 * KB + threadIdx.x];
+  int row[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) row[m] = g.perm[start + min(16 * m + ln, count - 1)];
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) issue(d);
-
-  // h rows -> e4m3 in LDS while the first weights travel: 16 lanes per row and group.
-  for (int q = threadIdx.x >> 4; q < count * KB; q += 16) {
-    const int r = q / KB, b = q - r * KB, l = threadIdx.x & 15, c = b * 128 + l * 8;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (c < K) load8(h, (size_t)(start + r) * K + c, 0, v);
+  __builtin_amdgcn_sched_barrier(0);
+  auto put_h = [&](int q, const float (&v)[8]) __attribute__((always_inline)) {
+    const int r = q / KB, b = q - r * KB;
     float mx = kAmaxMin;
 #pragma unroll
     for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
 #pragma unroll
     for (int d = 8; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+    if (q >= count * KB) return;
     const float inv = kE4M3Max * (1.0f / mx);
     *reinterpret_cast<u32x2*>(act + b * (AR * 128) + r * 128 + (((l >> 1) ^ ((r >> 1) & 7)) * 16) + (l & 1) * 8) =
         u32x2{pack_fp8x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
               pack_fp8x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
     if (l == 0) sx[b * AR + r] = mx / kE4M3Max;
-  }
-  const int blk0 = n0 / 128, nb = (min(n0 + tiles * 16, g.N) + 127) / 128 - blk0;
-  for (int q = threadIdx.x; q < nb * KB; q += 256) sw[q] = ws[(size_t)blk0 * KB + q];
-  size_t row[MT];
+  };
 #pragma unroll
-  for (int m = 0; m < MT; ++m) row[m] = g.perm[start + min(16 * m + ln, count - 1)];
+  for (int i = 0; i < HP; ++i) put_h(i * 16 + (threadIdx.x >> 4), hv[i]);
+  for (int q0 = HP * 16; q0 < count * KB; q0 += 16) {
+    float v[8];
+    load_h(q0 + (threadIdx.x >> 4), v);
+    put_h(q0 + (threadIdx.x >> 4), v);
+  }
+  if ((int)threadIdx.x < nb * KB) sw[threadIdx.x] = swv;
+  for (int q = 256 + threadIdx.x; q < nb * KB; q += 256) sw[q] = ws[(size_t)blk0 * KB + q];
   // LDS writes of every wave done; the ring's loads stay in flight.
   __builtin_amdgcn_s_waitcnt(0xc07f);
   f8_barrier();
@@ -426,29 +449,16 @@ __global__ __launch_bounds__(256) void f8_down_kernel(F8Args g, const float* h, 
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-      if (16 * m + ln < count) f8_store4(g, row[m], n + 4 * lg, acc[m]);
+      if (16 * m + ln < count) f8_store4(g, (size_t)row[m], n + 4 * lg, acc[m]);
   }
   wait_vmcnt<0>();
 }
 
-// ---- one token ----
-// A single token needs no sort and no sum over workgroups: gate_up works per pair on x
-// quantised in each workgroup, and down per 8 output rows over all pairs, so the whole call
-// is two launches.
-struct TokenArgs {
-  const uint16_t* x;     // [H] bf16
-  const int32_t* ids;    // [topk]
-  const float* weights;  // [topk]
-  const uint8_t* w;      // gate_up, or down, of expert e at w + e * w_stride
-  size_t w_stride;
-  uint32_t w_bytes;
-  const float* ws;
-  size_t ws_stride;
-  int H, I, HB, IB, E, first, topk;
-  float* h;              // [topk, I] fp32
-  void* out;
-  int out_f32;
-};
+// ---- one activation row ----
+// A single row leaves the matrix instructions with one column in sixteen, so these kernels
+// multiply in the vector unit, straight from registers: a 16-byte load per lane covers 8
+// weight rows x 128 bytes (8 whole lines), lane l holding 16 K elements of row l / 8, and
+// each lane keeps NB such loads in flight.  The row of x sits in LDS in its 8-bit form.
 
 // Eight values -> e4m3 with the scale of the 16 lanes that share a group.
 __device__ __forceinline__ u32x2 quant8(const float (&v)[8], float& scale) {
@@ -463,184 +473,280 @@ __device__ __forceinline__ u32x2 quant8(const float (&v)[8], float& scale) {
                pack_fp8x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
 }
 
-// The same activation row in all 16 columns: block of 128 values at p.
-__device__ __forceinline__ frag_bf16 row_frag(const char* p, int lg) {
-  i32x8 v;
-  const u32x4 lo = *reinterpret_cast<const u32x4*>(p + lg * 16), hi = *reinterpret_cast<const u32x4*>(p + 64 + lg * 16);
+// One row of K bf16 values to e4m3 and scales in LDS, by a workgroup of 256 threads, in two
+// halves: the loads, and, once the weights' loads are out too, the rest (loads complete in
+// order, so a load issued behind the weights would wait for them).  The tail of the last
+// block is filled with zeros.
+struct RowLoad {
+  u32x4 v[kTokenBlocks / 16];
+};
+__device__ __forceinline__ void row_load(RowLoad& r, const void* x, int K) {
+#pragma unroll
+  for (int i = 0; i < kTokenBlocks / 16; ++i) {
+    const int c = i * 2048 + (int)threadIdx.x * 8;
+    r.v[i] = c < K ? ld16(reinterpret_cast<const uint16_t*>(x) + c) : u32x4{0, 0, 0, 0};
+  }
+}
+__device__ __forceinline__ void row_to_lds(const RowLoad& r, int KB, char* x8, float* sx) {
+#pragma unroll
+  for (int i = 0; i < kTokenBlocks / 16; ++i) {
+    const int b = i * 16 + (threadIdx.x >> 4);
+    if (b >= KB) break;
+    float v[8], sc;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = bf_lo(r.v[i][q]);
+      v[2 * q + 1] = bf_hi(r.v[i][q]);
+    }
+    *reinterpret_cast<u32x2*>(x8 + i * 2048 + threadIdx.x * 8) = quant8(v, sc);
+    if ((threadIdx.x & 15) == 0) sx[b] = sc;
+  }
+}
+
+// Sum of 16 products of e4m3 values (exact in fp32) in fp32.
+__device__ __forceinline__ float dot16(u32x4 w, u32x4 x) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  float a = 0.f, b = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] = (int)lo[i];
-    v[4 + i] = (int)hi[i];
+    const f32x2 w0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false), w1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+    const f32x2 x0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[i], false), x1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[i], true);
+    a = fmaf(w0[0], x0[0], a);
+    b = fmaf(w0[1], x0[1], b);
+    a = fmaf(w1[0], x1[0], a);
+    b = fmaf(w1[1], x1[1], b);
   }
-  return widen(v);
+  return a + b;
 }
 
-// Workgroup (b, j): features 8 b .. 8 b + 7 of pair j.  One 16-row weight tile: 8 gate rows,
-// then the matching up rows; the four waves take the K blocks in turn.
-template <int STAGES>
-__global__ __launch_bounds__(256) void f8_token_gate_up_kernel(TokenArgs a) {
-  constexpr int WAVES = 4, RING = WAVES * STAGES * 2048;
-  __shared__ __attribute__((aligned(1024))) char lds[RING + kTokenBlocks * (128 + 12)];
-  char* x8 = lds + RING;
-  float* sx = reinterpret_cast<float*>(lds + RING + kTokenBlocks * 128);
-  float* sw = sx + kTokenBlocks;  // gate scales, then up scales
+// Sum over the 8 lanes that share a weight row.
+__device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor(v, 1);
+  v += __shfl_xor(v, 2);
+  return v + __shfl_xor(v, 4);
+}
+
+struct TokenArgs {
+  const void* x;         // bf16 [H] (projection: bf16, or e4m3 with xs)
+  const float* xs;
+  const int32_t* ids;    // [topk]
+  const float* weights;  // [topk]
+  const uint8_t* w;      // gate_up, or down, of expert e at w + e * w_stride
+  size_t w_stride;
+  uint32_t w_bytes;
+  const float* ws;
+  size_t ws_stride;
+  int H, I, HB, IB, E, first, topk;
+  float* h;              // [topk, I] fp32
+  void* out;
+  int out_f32;
+};
+
+// GU: workgroup (b, j) makes features 8 b .. 8 b + 7 of pair j's h from 8 gate rows and 8 up
+// rows of H elements.  Otherwise output rows 8 b .. 8 b + 7 of a projection of x [H] (I: the
+// number of outputs).  The four waves take the K blocks in turn; their sums are added in
+// wave order.
+template <bool GU, int NB>
+__global__ __launch_bounds__(256, 4) void f8_row_kernel(TokenArgs a) {
+  constexpr int WAVES = 4, P = GU ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) char x8[kTokenBlocks * 128];
+  __shared__ float sx[kTokenBlocks], sw[P][kTokenBlocks], red[WAVES][P][8];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lg = lane >> 4, lr = lane >> 3;
-  const int pair = blockIdx.y, f0 = blockIdx.x * 8, K = a.H, KB = a.HB;
-  const int expert = local_expert(a.ids[pair], a.first, a.E);
-  if (expert < 0) return;
-  const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (size_t)expert * a.w_stride, a.w_bytes);
-  char* my = lds + wave * (STAGES * 2048);
-  int ch[2];
-  uint32_t wo[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    ch[q] = (lane & 7) ^ (((8 * q + lr) >> 1) & 7);
-    wo[q] = (uint32_t)(q * a.I + f0 + lr) * (uint32_t)K + ch[q] * 16;
+  const int f0 = blockIdx.x * 8, K = a.H, KB = a.HB;
+  int expert = 0;
+  if (GU) {
+    expert = local_expert(a.ids[blockIdx.y], a.first, a.E);
+    if (expert < 0) return;
   }
-  const int nst = (KB + WAVES - 1) / WAVES;
-  auto issue = [&](int slot, int i) {
-    const int k = (i * WAVES + wave) * 128;
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      buf_ld_lds_nt(wr, my + slot * 2048 + q * 1024, k + ch[q] * 16 < K ? wo[q] + (uint32_t)k : kNoRow);
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (size_t)expert * a.w_stride, a.w_bytes);
+  const int ch = (lane & 7) * 16;
+  const uint32_t wo = (uint32_t)(f0 + (lane >> 3)) * (uint32_t)K + ch;
+  const uint32_t up = GU ? (uint32_t)a.I * (uint32_t)K : 0u;
+  // Unit u of this wave: block (u / P) * WAVES + wave of the gate (or only) or the up rows.
+  const int units = P * ((KB - wave + WAVES - 1) / WAVES);
+  u32x4 v[NB];
+  auto load = [&](int u) {
+    const int k = ((u / P) * WAVES + wave) * 128;
+    return buf_ld_nt(wr, k + ch < K ? wo + (uint32_t)(u % P) * up + (uint32_t)k : kNoRow);
   };
+  static_assert(NB % P == 0, "a buffer slot stays with the gate or the up rows");
+  // x and the scales first, then the weights, then x's 8-bit form.
+  const bool given = !GU && a.xs;
+  RowLoad x;
+  u32x4 xq[kTokenBlocks / 32];
+  float xsv = 0.f, wsv[P];
+  const int b0 = min((int)threadIdx.x, KB - 1);
+  if (given) {
 #pragma unroll
-  for (int st = 0; st < STAGES - 1; ++st) issue(st, st);
-  for (int b = threadIdx.x >> 4; b < KB; b += 16) {
-    const int l = threadIdx.x & 15, c = b * 128 + l * 8;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sc;
-    if (c < K) load8(a.x, c, 1, v);
-    *reinterpret_cast<u32x2*>(x8 + c) = quant8(v, sc);
-    if (l == 0) sx[b] = sc;
+    for (int i = 0; i < kTokenBlocks / 32; ++i) {
+      const int c = i * 4096 + (int)threadIdx.x * 16;
+      xq[i] = c < K ? ld16(static_cast<const char*>(a.x) + c) : u32x4{0, 0, 0, 0};
+    }
+    xsv = a.xs[b0];
+  } else {
+    row_load(x, a.x, K);
   }
   const float* ws = a.ws + (size_t)expert * a.ws_stride + (size_t)(f0 / 128) * KB;
-  for (int q = threadIdx.x; q < 2 * KB; q += 256)
-    sw[(q < KB ? 0 : kTokenBlocks - KB) + q] = ws[q < KB ? q : (size_t)a.IB * KB + q - KB];
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // LDS writes done; the ring's loads stay in flight
-  f8_barrier();
-
-  f32x4 acc{0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < nst; ++i) {
-    issue((i + STAGES - 1) % STAGES, i + STAGES - 1);
-    wait_vmcnt<2 * (STAGES - 1)>();
-    asm volatile("" ::: "memory");
-    const int kb = min(i * WAVES + wave, KB - 1);  // past K the weights are zeros
-    const frag_bf16 wf = widen(lds_frag(my + (i % STAGES) * 2048, lane));
-    const f32x4 p = mfma_widened(wf, row_frag(x8 + kb * 128, lg));
-    const float s = sx[kb] * sw[(lg >> 1) * kTokenBlocks + kb];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = fmaf(p[j], s, acc[j]);
-    __builtin_amdgcn_s_waitcnt(0xc07f);
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
+  for (int q = 0; q < P; ++q) wsv[q] = ws[(size_t)q * a.IB * KB + b0];
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < NB; ++i) v[i] = load(i);
+  __builtin_amdgcn_sched_barrier(0);
+  if (given) {
+#pragma unroll
+    for (int i = 0; i < kTokenBlocks / 32; ++i) *reinterpret_cast<u32x4*>(x8 + i * 4096 + threadIdx.x * 16) = xq[i];
+    if ((int)threadIdx.x < KB) sx[threadIdx.x] = xsv;
+  } else {
+    row_to_lds(x, KB, x8, sx);
   }
-  wait_vmcnt<0>();
-  __syncthreads();
-  f32x4* red = reinterpret_cast<f32x4*>(lds);
-  red[wave * 64 + lane] = acc;
-  __syncthreads();
-  if (wave != 0) return;
 #pragma unroll
-  for (int v = 1; v < WAVES; ++v) acc += red[v * 64 + lane];
-  f32x4 hv;
+  for (int q = 0; q < P; ++q)
+    if ((int)threadIdx.x < KB) sw[q][threadIdx.x] = wsv[q];
+  __syncthreads();
+
+  float acc[P];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) hv[j] = silu_mul(acc[j], __shfl_xor(acc[j], 32));  // up rows sit 32 lanes on
-  if ((lane & 15) == 0 && lg < 2) *reinterpret_cast<f32x4*>(a.h + (size_t)pair * a.I + f0 + 4 * lg) = hv;
+  for (int q = 0; q < P; ++q) acc[q] = 0.f;
+  // Units past the last are zeros.
+  auto use = [&](int u, int i) __attribute__((always_inline)) {
+    const int kb = min((u / P) * WAVES + wave, KB - 1);
+    const float p = dot16(v[i], *reinterpret_cast<const u32x4*>(x8 + kb * 128 + ch));
+    acc[i % P] = fmaf(p, sx[kb] * sw[i % P][kb], acc[i % P]);
+  };
+  int u0 = 0;
+  for (; u0 + NB < units; u0 += NB) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      use(u0 + i, i);
+      v[i] = load(u0 + NB + i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) use(u0 + i, i);
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    const float s = row_sum(acc[q]);
+    if ((lane & 7) == 0) red[wave][q][lane >> 3] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 8 || f0 + (int)threadIdx.x >= a.I) return;
+  float s[P];
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    s[q] = red[0][q][threadIdx.x];
+#pragma unroll
+    for (int v2 = 1; v2 < WAVES; ++v2) s[q] += red[v2][q][threadIdx.x];
+  }
+  const int n = f0 + threadIdx.x;
+  if (GU) a.h[(size_t)blockIdx.y * a.I + n] = silu_mul(s[0], s[P - 1]);
+  else if (a.out_f32) reinterpret_cast<float*>(a.out)[n] = s[0];
+  else reinterpret_cast<uint16_t*>(a.out)[n] = (uint16_t)f2bf(s[0]);
 }
 
-// Workgroup b: output rows 8 b .. 8 b + 7.  Wave w sums pairs w, w + 4, ... over the whole K
-// through a ring of D blocks of 8 rows x 128 bytes; the waves' sums are added in wave order.
-template <int D>
-__global__ __launch_bounds__(256) void f8_token_down_kernel(TokenArgs a) {
-  constexpr int WAVES = 4, RING = WAVES * D * 1024;
-  __shared__ __attribute__((aligned(1024))) char lds[RING + kTokenPairBlocks * (128 + 8)];
+// Down product of one token and the sum over its pairs.  Workgroup b: output rows 8 b .. + 7;
+// wave w takes pairs w, w + 4, ... with the whole K; the waves' sums are added in wave order.
+template <int NB>
+__global__ __launch_bounds__(256, 4) void f8_token_down_kernel(TokenArgs a) {
+  constexpr int WAVES = 4;
+  __shared__ __attribute__((aligned(16))) char h8[kTokenPairBlocks * 128];
+  __shared__ float sc[kTokenPairBlocks], sw[kTokenPairBlocks], red[WAVES][8];
   __shared__ int expert_of[SMLP_MAX_TOPK];
-  char* h8 = lds + RING;
-  float* sh = reinterpret_cast<float*>(lds + RING + kTokenPairBlocks * 128);
-  float* sw = sh + kTokenPairBlocks;
+  __shared__ float wt[SMLP_MAX_TOPK];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int ln = lane & 15, lg = lane >> 4, lr = lane >> 3;
   const int n0 = blockIdx.x * 8, K = a.I, KB = a.IB;
-  if ((int)threadIdx.x < a.topk) expert_of[threadIdx.x] = local_expert(a.ids[threadIdx.x], a.first, a.E);
-  __syncthreads();
-  char* my = lds + wave * (D * 1024);
-  const int ch = (lane & 7) ^ ((lr >> 1) & 7);
-  const uint32_t wo = (uint32_t)(n0 + lr) * (uint32_t)K + ch * 16;
-  // The local pairs of this wave, in order: next one at or after j.
-  auto next_pair = [&](int j) {
-    while (j < a.topk && __builtin_amdgcn_readfirstlane(expert_of[j]) < 0) j += WAVES;
-    return j;
-  };
-  auto rsrc_of = [&](int j) {
-    const int e = j < a.topk ? __builtin_amdgcn_readfirstlane(expert_of[j]) : 0;
-    return make_rsrc(a.w + (size_t)e * a.w_stride, j < a.topk ? a.w_bytes : 0u);
-  };
-  int ij = next_pair(wave), ikb = 0;
-  __amdgpu_buffer_rsrc_t wr = rsrc_of(ij);
-  auto issue = [&](int slot) __attribute__((always_inline)) {
-    const int k = ikb * 128;
-    buf_ld_lds_nt(wr, my + slot * 1024, k + ch * 16 < K ? wo + (uint32_t)k : kNoRow);
-    if (++ikb == KB) {
-      ikb = 0;
-      ij = next_pair(ij < a.topk ? ij + WAVES : ij);
-      wr = rsrc_of(ij);
-    }
-  };
+  // h first (its loads do not wait for the weights'), then ids, scales and weights.
+  constexpr int HP = kTokenPairBlocks / 16;
+  float hv[HP][8];
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) issue(d);
-  for (int q = threadIdx.x >> 4; q < a.topk * KB; q += 16) {
-    const int j = q / KB, b = q - j * KB, l = threadIdx.x & 15, c = b * 128 + l * 8;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sc;
-    if (c < K && expert_of[j] >= 0) load8(a.h, (size_t)j * K + c, 0, v);
-    *reinterpret_cast<u32x2*>(h8 + q * 128 + l * 8) = quant8(v, sc);
-    if (l == 0) {
-      sh[q] = sc;
-      sw[q] = expert_of[j] < 0 ? 0.f : a.ws[(size_t)expert_of[j] * a.ws_stride + (size_t)(n0 / 128) * KB + b];
+  for (int i = 0; i < HP; ++i) {
+    const int q = i * 16 + (threadIdx.x >> 4), j = q / KB, c = (q - j * KB) * 128 + (threadIdx.x & 15) * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) hv[i][e] = 0.f;
+    if (q < a.topk * KB && c < K) load8(a.h, (size_t)j * K + c, 0, hv[i]);
+  }
+  if ((int)threadIdx.x < a.topk) {
+    expert_of[threadIdx.x] = local_expert(a.ids[threadIdx.x], a.first, a.E);
+    wt[threadIdx.x] = a.weights[threadIdx.x];
+  }
+  __syncthreads();
+  float wsv = 0.f;
+  if ((int)threadIdx.x < a.topk * KB) {
+    const int j = threadIdx.x / KB, e = expert_of[j];
+    if (e >= 0) wsv = a.ws[(size_t)e * a.ws_stride + (size_t)(n0 / 128) * KB + threadIdx.x - j * KB];
+  }
+  const int ch = (lane & 7) * 16;
+  const uint32_t wo = (uint32_t)(n0 + (lane >> 3)) * (uint32_t)K + ch;
+  // Unit u of this wave: block u % KB of pair wave + WAVES * (u / KB); a pair of another rank
+  // reads nothing.
+  const int units = a.topk > wave ? KB * ((a.topk - wave + WAVES - 1) / WAVES) : 0;
+  int lj = wave, lkb = 0;
+  u32x4 v[NB];
+  auto load = [&]() {
+    const int e = lj < a.topk ? __builtin_amdgcn_readfirstlane(expert_of[lj]) : -1;
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (size_t)max(e, 0) * a.w_stride, e < 0 ? 0u : a.w_bytes);
+    const int k = lkb * 128;
+    const u32x4 r = buf_ld_nt(wr, k + ch < K ? wo + (uint32_t)k : kNoRow);
+    if (++lkb == KB) {
+      lkb = 0;
+      lj += WAVES;
+    }
+    return r;
+  };
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < NB; ++i) v[i] = load();
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < HP; ++i) {
+    const int q = i * 16 + (threadIdx.x >> 4);
+    float s;
+    const u32x2 v8 = quant8(hv[i], s);  // rows of other ranks' pairs hold anything and are not summed
+    if (q < a.topk * KB) {
+      *reinterpret_cast<u32x2*>(h8 + q * 128 + (threadIdx.x & 15) * 8) = v8;
+      if ((threadIdx.x & 15) == 0) sc[q] = s;
     }
   }
-  __builtin_amdgcn_s_waitcnt(0xc07f);
-  f8_barrier();
+  if ((int)threadIdx.x < a.topk * KB) sw[threadIdx.x] = wsv;
+  __syncthreads();
 
-  f32x4 sum{0.f, 0.f, 0.f, 0.f};
-  int slot = 0;
-  for (int j = next_pair(wave); j < a.topk; j = next_pair(j + WAVES)) {
-    f32x4 acc{0.f, 0.f, 0.f, 0.f};
-    for (int kb = 0; kb < KB; ++kb) {
-      issue(slot == 0 ? D - 1 : slot - 1);
-      wait_vmcnt<D - 1>();
-      asm volatile("" ::: "memory");
-      const frag_bf16 wf = widen(act_frag(my + slot * 1024, ln & 7, lg));
-      const int q = j * KB + kb;
-      const f32x4 p = mfma_widened(wf, row_frag(h8 + q * 128, lg));
-      const float s = sh[q] * sw[q];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(p[i], s, acc[i]);
-      __builtin_amdgcn_s_waitcnt(0xc07f);
-      __builtin_amdgcn_sched_barrier(0);
-      asm volatile("" ::: "memory");
-      slot = slot == D - 1 ? 0 : slot + 1;
+  float sum = 0.f, acc = 0.f;
+  int j = wave, kb = 0;
+  // Blocks past the last are zeros; a finished pair's sum is weighted and restarted.
+  auto use = [&](int i) __attribute__((always_inline)) {
+    const int q = min(j * KB + kb, a.topk * KB - 1);
+    acc = fmaf(dot16(v[i], *reinterpret_cast<const u32x4*>(h8 + q * 128 + ch)), sc[q] * sw[q], acc);
+    if (++kb == KB) {
+      if (j < a.topk && __builtin_amdgcn_readfirstlane(expert_of[j]) >= 0) sum = fmaf(wt[j], acc, sum);
+      acc = 0.f;
+      kb = 0;
+      j += WAVES;
     }
-    const float wt = a.weights[j];
+  };
+  int u0 = 0;
+  for (; u0 + NB < units; u0 += NB) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] = fmaf(wt, acc[i], sum[i]);
+    for (int i = 0; i < NB; ++i) {
+      use(i);
+      v[i] = load();
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
-  wait_vmcnt<0>();
-  __syncthreads();
-  f32x4* red = reinterpret_cast<f32x4*>(lds);
-  red[wave * 64 + lane] = sum;
-  __syncthreads();
-  if (wave != 0) return;
 #pragma unroll
-  for (int v = 1; v < WAVES; ++v) sum += red[v * 64 + lane];
-  if (ln != 0 || lg >= 2) return;  // rows 8 .. 15 of the tile repeat rows 0 .. 7
-  const int n = n0 + 4 * lg;
-  if (a.out_f32) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + n) = sum;
-  else
-    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + n) =
-        u32x2{pack_bf2(sum[0], sum[1]), pack_bf2(sum[2], sum[3])};
+  for (int i = 0; i < NB; ++i) use(i);
+  sum = row_sum(sum);
+  if ((lane & 7) == 0) red[wave][lane >> 3] = sum;
+  __syncthreads();
+  if (threadIdx.x >= 8) return;
+  float s = red[0][threadIdx.x];
+#pragma unroll
+  for (int v2 = 1; v2 < WAVES; ++v2) s += red[v2][threadIdx.x];
+  const int n = n0 + threadIdx.x;
+  if (a.out_f32) reinterpret_cast<float*>(a.out)[n] = s;
+  else reinterpret_cast<uint16_t*>(a.out)[n] = (uint16_t)f2bf(s);
 }
 
 // Workgroup -> (tile_m, tile_n): each XCD (workgroups are handed out round-robin over the 8)
@@ -1239,6 +1345,24 @@ int launch_quant_fp8(const void* x, int bf16, int64_t parts, int64_t rows, int64
   return (int)hipGetLastError();
 }
 
+int launch_row_fp8(const void* x, const float* xs, const void* w, const float* ws, void* y, int64_t K, int64_t N,
+                   int out_f32, hipStream_t s) {
+  TokenArgs t{};
+  t.x = x;
+  t.xs = xs;
+  t.w = static_cast<const uint8_t*>(w);
+  t.w_bytes = (uint32_t)(N * K);
+  t.ws = ws;
+  t.H = (int)K;
+  t.I = (int)N;
+  t.HB = (int)((K + 127) / 128);
+  t.IB = (int)((N + 127) / 128);
+  t.out = y;
+  t.out_f32 = out_f32;
+  hipLaunchKernelGGL((f8_row_kernel<false, 14>), dim3((unsigned)((N + 7) / 8)), dim3(256), 0, s, t);
+  return (int)hipGetLastError();
+}
+
 int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t as_row, int64_t as_kb,
                       const void* w, const float* ws, void* y, int64_t M, int64_t K, int64_t N, int64_t ldy,
                       int out_f32, float* part, hipStream_t s) {
@@ -1301,7 +1425,7 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
 
   if (p.token) {
     TokenArgs t{};
-    t.x = static_cast<const uint16_t*>(c.x);
+    t.x = c.x;
     t.ids = c.ids;
     t.weights = c.weights;
     t.w = static_cast<const uint8_t*>(c.w_gate_up);
@@ -1319,7 +1443,7 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
     t.h = h32;
     t.out = c.out;
     t.out_f32 = c.out_f32;
-    hipLaunchKernelGGL((f8_token_gate_up_kernel<5>), dim3((unsigned)(p.I / 8), (unsigned)p.topk), dim3(256), 0, s, t);
+    hipLaunchKernelGGL((f8_row_kernel<true, 14>), dim3((unsigned)(p.I / 8), (unsigned)p.topk), dim3(256), 0, s, t);
     int rc = (int)hipGetLastError();
     if (rc) return rc;
     t.w = static_cast<const uint8_t*>(c.w_down);
@@ -1327,7 +1451,7 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
     t.w_bytes = (uint32_t)(p.H * p.I);
     t.ws = c.s_down;
     t.ws_stride = (size_t)(HB * IB);
-    hipLaunchKernelGGL((f8_token_down_kernel<6>), dim3((unsigned)(p.H / 8)), dim3(256), 0, s, t);
+    hipLaunchKernelGGL((f8_token_down_kernel<12>), dim3((unsigned)(p.H / 8)), dim3(256), 0, s, t);
     return (int)hipGetLastError();
   }
   PrepArgs pa{};

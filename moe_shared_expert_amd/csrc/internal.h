@@ -140,8 +140,12 @@ int launch_bf16_to_f16(const void* src, int64_t ld_src, int64_t rows, int64_t co
 int launch_route(const void* logits, int bf16, int64_t T, int64_t E, int64_t ldl, const float* bias,
                  const smlp_route& r, int32_t* ids, float* weights, hipStream_t s);
 
+// Limits of the short-K down kernel (16-row weight tiles per workgroup) and of the kernels
+// for one token (blocks of 128 in H; blocks of 128 in I over all pairs).
+constexpr int kDownRun = 496, kTokenBlocks = 64, kTokenPairBlocks = 64;
+
 // One 8-bit block-scaled product (fp8.hip).
-enum { F8_KIND_STREAM = 0, F8_KIND_TILE = 1, F8_KIND_DOWN = 2 };
+enum { F8_KIND_STREAM = 0, F8_KIND_TILE = 1, F8_KIND_DOWN = 2, F8_KIND_ROW = 3 };
 struct F8Plan {
   int kind;
   int bm;                     // activation rows per tile
@@ -157,13 +161,12 @@ struct F8Plan {
 // (dense [parts, row blocks, column blocks]) and 128 columns.
 int launch_quant_fp8(const void* x, int bf16, int64_t parts, int64_t rows, int64_t cols, int64_t ldx,
                      int block_rows, void* q, float* scales, int64_t s_row, int64_t s_kb, hipStream_t s);
+// The product for one row (K <= 128 * kTokenBlocks): x bf16 (xs null) or e4m3 with scales.
+int launch_row_fp8(const void* x, const float* xs, const void* w, const float* ws, void* y, int64_t K, int64_t N,
+                   int out_f32, hipStream_t s);
 int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t as_row, int64_t as_kb,
                       const void* w, const float* ws, void* y, int64_t M, int64_t K, int64_t N, int64_t ldy,
                       int out_f32, float* part, hipStream_t s);
-
-// Limits of the short-K down kernel (16-row weight tiles per workgroup) and of the kernels
-// for one token (blocks of 128 in H; blocks of 128 in I over all pairs).
-constexpr int kDownRun = 496, kTokenBlocks = 64, kTokenPairBlocks = 64;
 
 // The routed experts: sort, gate_up, (requantisation of h,) down, weighted sum (fp8.hip).
 struct ExpertsPlan {

@@ -86,7 +86,11 @@ int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, L
     return fail(SMLP_ERR_SHAPE, "M*K, N*K and M*N must be below 2^31");
   LinearF8Plan p{};
   const int64_t KB = blocks128(K);
-  if (M <= 32) {
+  if (M == 1 && KB <= smlp::kTokenBlocks) {
+    p.f = stream_plan(M, KB);
+    p.f.kind = smlp::F8_KIND_ROW;  // x is brought to its 8-bit form in each workgroup
+    x_fp8 = 1;
+  } else if (M <= 32) {
     p.f = stream_plan(M, KB);
   } else {
     const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256), t128 = blocks128(M) * blocks128(N);
@@ -287,6 +291,11 @@ int shared_mlp_linear_fp8(const void* x, const float* x_scales, const void* w, c
     if (overlap(yr, q) || overlap(wsr, q)) return fail(SMLP_ERR_ALIAS, "y or the workspace overlaps an input");
   if (overlap(yr, wsr)) return fail(SMLP_ERR_ALIAS, "y overlaps the workspace");
   (void)hipGetLastError();
+  if (p.f.kind == smlp::F8_KIND_ROW) {
+    rc = smlp::launch_row_fp8(x, x_scales, w, w_scales, y, K, N, out_fp32, stream);
+    if ((rc = hip_status(rc, "8-bit product launch"))) return rc;
+    return ok();
+  }
   char* base = static_cast<char*>(workspace);
   const void* x8 = x;
   const float* xs = x_scales;

@@ -23,6 +23,9 @@ int launch_quant_fp8(const void*, int, int64_t, int64_t, int64_t, int64_t, int, 
                      hipStream_t) {
   return ++g_launches, 0;
 }
+int launch_row_fp8(const void*, const float*, const void*, const float*, void*, int64_t, int64_t, int, hipStream_t) {
+  return ++g_launches, 0;
+}
 int launch_linear_fp8(const F8Plan&, const void*, const float*, int64_t, int64_t, const void*, const float*, void*,
                       int64_t, int64_t, int64_t, int64_t, int, float*, hipStream_t) {
   return ++g_launches, 0;

@@ -148,7 +148,8 @@ def test_experts_refusals(L, kw, status):
 
 def test_workspace_sizes(L):
     assert binding.shared_mlp_linear_fp8_workspace_bytes(0, 256, 64, False) == 0
-    for M in (1, 17, 100, 5000):
+    assert binding.shared_mlp_linear_fp8_workspace_bytes(1, 7168, 2112, False) == 0
+    for M in (2, 17, 100, 5000):
         assert binding.shared_mlp_linear_fp8_workspace_bytes(M, 7168, 2112, False) >= M * (7168 + 4 * 56)
     small = binding.shared_mlp_experts_fp8_workspace_bytes(1, 7168, 768, 128, 8)
     big = binding.shared_mlp_experts_fp8_workspace_bytes(8192, 7168, 768, 128, 8)
