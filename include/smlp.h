@@ -313,8 +313,8 @@ int shared_mlp_experts_fp8_workspace_bytes(int64_t T, int64_t H, int64_t I, int6
  *   w_gate_up   e4m3 [E, 2 I, H] (gate rows, then up rows), s_gate_up [E, 2 ceil(I / 128),
  *               ceil(H / 128)]: the row blocks of the gate rows, then those of the up rows
  *   w_down      e4m3 [E, H, I], s_down [E, ceil(H / 128), ceil(I / 128)]
- *   out         [T, H] bf16 (rounded once; each expert's y may be rounded to bf16 before the
- *               fp32 sum where the tiled kernels run) or fp32 (partial_fp32 != 0)
+ *   out         [T, H] bf16 (rounded once; with many tokens each expert's y passes through
+ *               fp16 with a common exponent per 64 columns) or fp32 (partial_fp32 != 0)
  *   workspace   >= shared_mlp_experts_fp8_workspace_bytes(...), 256-byte aligned
  * H and I positive multiples of 16; E in [1, SMLP_MAX_EXPERTS]; topk in [1, SMLP_MAX_TOPK];
  * T * H, T * topk, T * topk * I and 2 * I * H < 2^31; x, w_gate_up, w_down and out 16-byte

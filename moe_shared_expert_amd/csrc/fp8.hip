@@ -47,11 +47,14 @@ struct F8Args {
   const int* hdr;      // experts: tile list (SortHeader layout below)
   const int* perm;     // experts: pair at each sorted position
   int topk;
-  void* out;           // projection: y; gate_up: h; down: y of each pair
+  void* out;           // projection: y; gate_up: h; down: y (rows: sorted positions)
   int ldo;
-  int out_f32;         // fp32 (1) or bf16 (0) output; gate_up: fp32 h (1) or e4m3 h (0)
+  int out_f32;         // fp32 (1) or bf16 (0) output; gate_up: fp32 h (1) or e4m3 h (0); down:
+                       // fp32 y (1) or fp16 y with exponents (0)
   float* hs;           // gate_up with e4m3 h: scales, block b of position p at hs[b * hs_ld + p]
   int hs_ld;
+  uint8_t* yexp;       // down with fp16 y: exponent of position p and columns 64 c .. + 63 at
+                       // yexp[c * hs_ld + p]
   float* part;         // projection with a K split: fp32 partials [slices][M][N]
   int kslice;          // K blocks per slice
 };
@@ -309,14 +312,11 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
       const int n = f0 + 16 * t + 4 * lg;
       if (n >= g.N) continue;
       f32x4 v = acc[t][m];
-      size_t row = start + r;
       if constexpr (GU) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = silu_mul(v[j], acc[t + FT][m][j]);
-      } else if (MODE == F8_DOWN) {
-        row = g.perm[start + r];
       }
-      f8_store4(g, row, n, v);
+      f8_store4(g, (size_t)(start + r), n, v);
     }
   }
 }
@@ -372,8 +372,7 @@ __global__ __launch_bounds__(256) void f8_down_kernel(F8Args g, const float* h, 
     }
   };
   // h rows -> e4m3 in LDS, 16 lanes per row and group of 128.  Loads complete in order, so
-  // the first HP rounds of h (and the scales and places of the results) are loaded ahead of
-  // the ring's weights; more rounds only come with more than HP * 16 / KB rows.
+  // the first HP rounds of h and the weight scales are loaded ahead of the ring's weights; more rounds only come with more than HP * 16 / KB rows.
   constexpr int HP = 3;
   const int l = threadIdx.x & 15;
   float hv[HP][8];
@@ -388,9 +387,6 @@ __global__ __launch_bounds__(256) void f8_down_kernel(F8Args g, const float* h, 
   const int blk0 = n0 / 128, nb = (min(n0 + tiles * 16, g.N) + 127) / 128 - blk0;
   float swv = 0.f;
   if ((int)threadIdx.x < nb * KB) swv = ws[(size_t)blk0 * KB + threadIdx.x];
-  int row[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) row[m] = g.perm[start + min(16 * m + ln, count - 1)];
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) issue(d);
@@ -449,7 +445,7 @@ __global__ __launch_bounds__(256) void f8_down_kernel(F8Args g, const float* h, 
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-      if (16 * m + ln < count) f8_store4(g, (size_t)row[m], n + 4 * lg, acc[m]);
+      if (16 * m + ln < count) f8_store4(g, (size_t)(start + 16 * m + ln), n + 4 * lg, acc[m]);
   }
   wait_vmcnt<0>();
 }
@@ -749,9 +745,10 @@ __global__ __launch_bounds__(256, 4) void f8_token_down_kernel(TokenArgs a) {
   else reinterpret_cast<uint16_t*>(a.out)[n] = (uint16_t)f2bf(s);
 }
 
-// Workgroup -> (tile_m, tile_n): each XCD (workgroups are handed out round-robin over the 8)
-// takes a contiguous run of the tiles, walked in groups of GROUP_M row tiles, so that the
-// workgroups resident on one XCD share weight and activation tiles in its L2.
+// Position `lin` of the launch order -> (tile_m, tile_n): each XCD (workgroups are handed out
+// round-robin over the 8) takes a contiguous run of the tiles, walked in groups of GROUP_M
+// row tiles, so that the workgroups resident on one XCD share weight and activation tiles in
+// its L2.
 __device__ __forceinline__ bool f8_coords(int tiles_m, int tiles_n, int lin, int& tm, int& tn) {
   constexpr int XCDS = 8, GROUP_M = 4;
   const int total = tiles_m * tiles_n;
@@ -768,75 +765,128 @@ __device__ __forceinline__ bool f8_coords(int tiles_m, int tiles_n, int lin, int
   return true;
 }
 
+// 16-byte, 4-byte and 1-byte stores through a buffer resource: one past its end is dropped.
+__device__ __forceinline__ void buf_st16(__amdgpu_buffer_rsrc_t r, uint32_t off, u32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, 2);
+}
+__device__ __forceinline__ void buf_st4(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t v) {
+  __builtin_amdgcn_raw_buffer_store_b32(v, r, (int)off, 0, 0);
+}
+__device__ __forceinline__ void buf_st1(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t v) {
+  __builtin_amdgcn_raw_buffer_store_b8((unsigned char)v, r, (int)off, 0, 0);
+}
+
 // LDS-tiled kernel: BM activation rows x BN weight rows (gate_up: BN / 2 features and
-// both their rows) per workgroup, WM x WN waves.  EXACT: products through bf16.
+// both their rows) per tile, WM x WN waves; a workgroup takes tiles lin, lin + gridDim.x, ...
+// EXACT: products through bf16.
 template <int BM, int BN, int WM, int WN, int NS, int MODE, bool EXACT>
 __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
   constexpr bool GU = MODE == F8_GATE_UP;
   constexpr int W = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr int FT = GU ? TN / 2 : TN;
-  constexpr int FN = GU ? BN / 2 : BN;  // features per workgroup
+  constexpr int FN = GU ? BN / 2 : BN;  // features per tile
   constexpr int AL = BM / 8 / W, BL = BN / 8 / W;
   constexpr int RPW = BM / W;  // activation rows whose scales a wave fetches
   static_assert(AL * W * 8 == BM && BL * W * 8 == BN && RPW <= 32, "tile / wave mismatch");
-  static_assert(!GU || (TN % 2 == 0 && FN == 128), "a gate_up workgroup covers one scale group of h");
+  static_assert(!GU || (TN % 2 == 0 && FN == 128), "a gate_up tile covers one scale group of h");
+  static_assert(MODE != F8_DOWN || 16 * TN == 64, "64 columns share an exponent");
   static_assert(BN / WN <= 128 && 128 % (16 * FT) == 0, "one weight scale per wave");
   constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   constexpr int STAGE = A_BYTES + B_BYTES + W * 256;
   constexpr int LPS = AL + BL + 1;
-  static_assert(NS >= 2 && LPS * (NS - 1) < 64, "loads in flight");
-  __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE];
+  static_assert(NS >= 2 && LPS * (NS - 1) < 40, "loads in flight");
+  // Results pass through a staging area of their own, so that the next tile's first loads
+  // can fill the ring meanwhile.
+  constexpr int PITCH = 32 * TN + 16;
+  constexpr int STAGING = W * 16 * PITCH;
+  static_assert(STAGING >= WN * BM * 4, "the row maxima of gate_up fit too");
+  constexpr int PERM = GU ? (BM < 64 * W ? BM : 64 * W) * 4 : 0;  // the next tile's pairs
+  __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE + STAGING + PERM];
+  static_assert(NS * STAGE + STAGING + PERM <= 160 * 1024, "LDS");
+  static_assert(!GU || BM % 64 == 0, "64 pairs per load");
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
   const int ln = lane & 15, lg = lane >> 4, lr = lane >> 3;
-  int tile_m, tile_n, expert, start, count;
   const int tiles_m = MODE == F8_LINEAR ? g.tiles_m : g.hdr[0];
-  if (!f8_coords(tiles_m, g.tiles_n, blockIdx.x, tile_m, tile_n)) return;
-  if (!f8_tile(g, MODE, BM, tile_m, expert, start, count)) return;
-  const int f0 = tile_n * FN;
   const int K = g.K;
   const int kb0 = blockIdx.y * g.kslice;
   const int nk = min(g.KB - kb0, g.kslice);
-  const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + (size_t)expert * g.w_stride, g.w_bytes);
   const __amdgpu_buffer_rsrc_t ar = make_rsrc(g.a, g.a_bytes);
 
   // Block i of this wave: tile rows (i * W + wave) * 8 .. + 7; this lane's row and chunk.
   static_assert(W % 2 == 0, "one chunk permutation for all blocks of a wave");
   const int chk = (lane & 7) ^ ((4 * wave + (lr >> 1)) & 7);
-  uint32_t aoff[AL], boff[BL];
-#pragma unroll
-  for (int i = 0; i < AL; ++i) {
-    const int r = (i * W + wave) * 8 + lr;
-    aoff[i] = r < count ? (uint32_t)f8_arow(g, MODE, start, r) * (uint32_t)K + chk * 16 : kNoRow;
-  }
-#pragma unroll
-  for (int i = 0; i < BL; ++i) {
-    const int r = (i * W + wave) * 8 + lr;
-    int f = f0 + r, row = f;
-    if (GU) {
-      // Each wave column's 16 * TN rows: its gate rows, then the matching up rows.
-      const int wc = r / (16 * TN), rr = r % (16 * TN);
-      f = f0 + wc * 16 * FT + rr % (16 * FT);
-      row = rr < 16 * FT ? f : g.N + f;
+
+  // A tile's place.
+  struct Place {
+    int expert, start, count, f0;
+  };
+  auto place = [&](int lin, Place& t) __attribute__((always_inline)) {
+    int tm, tn;
+    if (!f8_coords(tiles_m, g.tiles_n, lin, tm, tn)) return false;
+    f8_tile(g, MODE, BM, tm, t.expert, t.start, t.count);
+    t.f0 = tn * FN;
+    return true;
+  };
+  // gate_up: the pairs of a tile's rows on their way to LDS (every wave one load).
+  int* const pairs = reinterpret_cast<int*>(lds + NS * STAGE + STAGING);
+  auto fetch_pairs = [&](const Place& t) __attribute__((always_inline)) {
+    if constexpr (GU) {
+      const int r0 = wave * 64 % BM;
+      glb_ld_lds4(g.perm + t.start + min(r0 + lane, t.count - 1), reinterpret_cast<char*>(pairs + r0));
     }
-    boff[i] = f < g.N ? (uint32_t)row * (uint32_t)K + chk * 16 : kNoRow;
-  }
-  // Scale source of this lane: lanes 0 .. RPW - 1 activation rows wave * RPW + lane, lanes
-  // 32 and up the block of this wave's weight rows (odd lanes: of its up rows).
+  };
+  // Activation row of tile row r.
+  auto arow = [&](const Place& t, int r) __attribute__((always_inline)) {
+    if constexpr (GU) return pairs[r] / g.topk;
+    else return t.start + min(r, t.count - 1);
+  };
+
+  uint32_t aoff[AL], boff[BL];
+  __amdgpu_buffer_rsrc_t wr;
   const float* sp;
   int sstep;
-  if (lane < 32) {
-    const int r = wave * RPW + lane % RPW;
-    sp = g.as + (size_t)f8_arow(g, MODE, start, min(r, count - 1)) * g.as_row;
-    sstep = g.as_kb;
-  } else {
-    const int blk = min((f0 + wn * 16 * FT) / 128, g.nblk - 1) + (GU && (lane & 1) ? g.nblk : 0);
-    sp = g.ws + (size_t)expert * g.ws_stride + (size_t)blk * g.KB;
-    sstep = 1;
-  }
+  // Lane number that the compiler takes for new in each tile: what is derived from it is
+  // computed again instead of being kept in registers through the product.
+  auto fresh = [&]() __attribute__((always_inline)) {
+    int l = threadIdx.x & 63;
+    asm volatile("" : "+v"(l));
+    return l;
+  };
+  auto aim = [&](const Place& t) __attribute__((always_inline)) {
+    const int lane = fresh(), lr = lane >> 3;
+    wr = make_rsrc(g.w + (size_t)t.expert * g.w_stride, g.w_bytes);
+#pragma unroll
+    for (int i = 0; i < AL; ++i)
+      aoff[i] = (i * W + wave) * 8 + lr < t.count ? (uint32_t)arow(t, (i * W + wave) * 8 + lr) * (uint32_t)K + chk * 16
+                                                  : kNoRow;
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
+      const int r = (i * W + wave) * 8 + lr;
+      int f = t.f0 + r, row = f;
+      if (GU) {
+        // Each wave column's 16 * TN rows: its gate rows, then the matching up rows.
+        const int wc = r / (16 * TN), rr = r % (16 * TN);
+        f = t.f0 + wc * 16 * FT + rr % (16 * FT);
+        row = rr < 16 * FT ? f : g.N + f;
+      }
+      boff[i] = f < g.N ? (uint32_t)row * (uint32_t)K + chk * 16 : kNoRow;
+    }
+    // Scale source of this lane: lanes 0 .. RPW - 1 activation rows wave * RPW + lane, lanes
+    // 32 and up the block of this wave's weight rows (odd lanes: of its up rows).
+    if (lane < 32) {
+      sp = g.as + (size_t)arow(t, wave * RPW + lane % RPW) * g.as_row;
+      sstep = g.as_kb;
+    } else {
+      const int blk = min((t.f0 + wn * 16 * FT) / 128, g.nblk - 1) + (GU && (lane & 1) ? g.nblk : 0);
+      sp = g.ws + (size_t)t.expert * g.ws_stride + (size_t)blk * g.KB;
+      sstep = 1;
+    }
+    sp += (size_t)kb0 * sstep;
+  };
 
   // Load l of the LPS per wave and step: activation blocks, weight blocks, scales.  Data past
   // the end of K arrives as zeros.  Steps are issued in order, so the scale pointer advances
@@ -853,227 +903,356 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
       sp += kb + 1 < g.KB ? sstep : 0;
     }
   };
-  auto issue = [&](int buf, int kb) {
+  auto issue = [&](int buf, int kb) __attribute__((always_inline)) {
 #pragma unroll
     for (int l = 0; l < LPS; ++l) issue_one(buf, kb, l);
   };
-  sp += (size_t)kb0 * sstep;
+  constexpr int SLOTS = TM * TN;
+  constexpr int Q = (LPS + SLOTS - 1) / SLOTS;       // loads per slot of the pinned schedule
+  constexpr int HALF = Q * TN < LPS ? Q * TN : LPS;  // loads issued in the last row tile
+  // Every step of the ring is issued, those past the slice too (they are not used, and past K
+  // they read nothing), so the loop has no branches and its waits are constants.
+  auto first_loads = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int st = 0; st < NS - 1; ++st) issue(st, kb0 + st);
+    if constexpr (!EXACT) {
+#pragma unroll
+      for (int l = 0; l < HALF; ++l) issue_one(NS - 1, kb0 + NS - 1, l);
+    }
+  };
+  constexpr int AHEAD = (NS - 2) * LPS + (EXACT ? 0 : HALF);  // loads behind step 0's
 
   f32x4 acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
   // Scale of row tile i in a stage: the fetching wave's region and place.
   auto row_scale = [&](const char* sc, int i) __attribute__((always_inline)) {
     const int r = (wm * TM + i) * 16 + ln;
     return *reinterpret_cast<const float*>(sc + (r / RPW) * 256 + (r % RPW) * 4);
   };
 
-  if constexpr (!EXACT) {
-    // Pinned schedule.  A step is TM x TN slots, row tile by row tile.  Slot m issues one
-    // matrix instruction and, while it runs, the four multiply-adds of slot m - 2, whose
-    // result has arrived by then; the fragments and scale of the next row tile are read
-    // during the present one.  The barrier that hands a stage back sits before the last row
-    // tile, whose operands every wave then holds in registers: that tile's matrix
-    // instructions cover the barrier, the reads of the next step's weights (each fragment
-    // right after its last use) and the first loads into the released stage; the remaining
-    // loads go out one per slot at the top of the next step.
-    constexpr int SLOTS = TM * TN;
-    static_assert(TM >= 2 && TM % 2 == 0 && SLOTS % 4 == 0, "fragment and result buffers alternate");
-    i32x8 wf[TN], af[2];
-    f32x4 p[4];
-    float sg[2] = {0.f, 0.f}, su[2] = {0.f, 0.f}, swg, swu;
-    p[2] = p[3] = f32x4{0.f, 0.f, 0.f, 0.f};  // the first step's slots 0 and 1 add nothing
-    auto madd = [&](int m) __attribute__((always_inline)) {
-      const int i = m / TN, j = m % TN;
-      const float sc = GU && j >= FT ? su[i & 1] : sg[i & 1];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[m & 3][e], sc, acc[i][j][e]);
-    };
-    auto read_af = [&](const char* st, int i, int half) __attribute__((always_inline)) {
-      lds_half(st + (wm * TM + i) * 2048, lane, half, af[i & 1]);
-    };
-    auto read_wf = [&](const char* st, int j) __attribute__((always_inline)) {
-      lds_half(st + A_BYTES + (wn * TN + j) * 2048, lane, 0, wf[j]);
-      lds_half(st + A_BYTES + (wn * TN + j) * 2048, lane, 1, wf[j]);
-    };
-    auto scales_of = [&](float s, int slot) __attribute__((always_inline)) {
-      sg[slot] = s * swg;
-      if constexpr (GU) su[slot] = s * swu;
-    };
-    constexpr int Q = (LPS + SLOTS - 1) / SLOTS;         // loads per slot
-    constexpr int HALF = Q * TN < LPS ? Q * TN : LPS;    // loads issued in the last row tile
-    // Slots of row tile i of a step (stage st); nst: the next step's stage (read in the last
-    // tile); loads l0 .. l1 - 1 of step lkb into stage lbuf go out Q per slot from the top.
-    auto row_tile = [&](int i, const char* st, const char* nst, int lbuf, int lkb, int l0, int l1)
-        __attribute__((always_inline)) {
-      const bool last = i == TM - 1;
-      const char* rst = last ? nst : st;
-      const int ri = last ? 0 : i + 1;
-      float s_next = 0.f, g_next = 0.f, u_next = 0.f;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int m = i * TN + j;
-        p[m & 3] = mfma_fp8(wf[j], af[i & 1]);
-        madd((m + SLOTS - 2) % SLOTS);
-        if (last) read_wf(nst, j);
-        if (j == 0) {
-          s_next = row_scale(rst + A_BYTES + B_BYTES, ri);
-          read_af(rst, ri, 0);
-          if (TN == 1) read_af(rst, ri, 1);
-        }
-        if (j == 1) read_af(rst, ri, 1);
-        if (last && j == TN - 1) {
-          const float* w2 = reinterpret_cast<const float*>(nst + A_BYTES + B_BYTES + wave * 256 + 128);
-          g_next = w2[0];
-          if constexpr (GU) u_next = w2[1];
-        }
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-          if (l0 + j * Q + q < l1) issue_one(lbuf, lkb, l0 + j * Q + q);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (last) {
-        swg = g_next;
-        swu = u_next;
-      }
-      scales_of(s_next, ri & 1);
-    };
-    // Every step of the ring is issued, those past the slice too (they are not used, and past
-    // K they read nothing), so the loop has no branches and its waits are constants.
-#pragma unroll
-    for (int st = 0; st < NS - 1; ++st) issue(st, kb0 + st);
-#pragma unroll
-    for (int l = 0; l < HALF; ++l) issue_one(NS - 1, kb0 + NS - 1, l);
-    wait_vmcnt<(NS - 2) * LPS + HALF>();
-    f8_barrier();
-    {
-      const char* st = lds;
-      const float* w2 = reinterpret_cast<const float*>(st + A_BYTES + B_BYTES + wave * 256 + 128);
-      swg = w2[0];
-      swu = GU ? w2[1] : 0.f;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) read_wf(st, j);
-      read_af(st, 0, 0);
-      read_af(st, 0, 1);
-      scales_of(row_scale(st + A_BYTES + B_BYTES, 0), 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    for (int kt = 0; kt < nk; ++kt) {
-      const int cur = kt % NS, nxt = (kt + 1) % NS;
-      const char* st = lds + cur * STAGE;
-      const char* nst = lds + nxt * STAGE;
-      // The rest of step kt + NS - 1's loads (its first HALF went out in the last row tile of
-      // the step before).
-#pragma unroll
-      for (int i = 0; i < TM - 1; ++i)
-        row_tile(i, st, nst, (kt + NS - 1) % NS, kb0 + kt + NS - 1, HALF + i * TN * Q, LPS);
-      static_assert(HALF + (TM - 1) * TN * Q >= LPS, "a step's slots hold its loads");
-      // Every wave holds the last row tile's operands (lgkmcnt 0) and step kt + 1 has landed.
-      // (After the last step the reads below fetch fragments that are never used.)
-      __builtin_amdgcn_s_waitcnt(0xc07f);
-      wait_vmcnt<(NS - 2) * LPS>();
-      f8_barrier();
-      row_tile(TM - 1, st, nst, cur, kb0 + kt + NS, 0, HALF);
-    }
+  int lin = blockIdx.x;
+  Place cur;
+  if (!place(lin, cur)) return;
+  if constexpr (GU) {
+    fetch_pairs(cur);
     wait_vmcnt<0>();
-    // The last two slots' multiply-adds; sg / su of the last row tile are still in place.
-    madd(SLOTS - 2);
-    madd(SLOTS - 1);
     f8_barrier();
-  } else {
+  }
+  aim(cur);
+  if constexpr (GU) {
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    f8_barrier();  // the pairs are read before the next tile's arrive
+  }
+  first_loads();
+  wait_vmcnt<AHEAD>();
+  for (;;) {
+    f8_barrier();  // step 0 has landed in every wave's view
+    // The next tile's place and pairs are looked up while this one is multiplied.
+    Place nxt_place;
+    const bool more = place(lin + (int)gridDim.x, nxt_place);
+    if (more) fetch_pairs(nxt_place);
 #pragma unroll
-    for (int st = 0; st < NS - 1; ++st)
-      if (st < nk) issue(st, kb0 + st);
-    for (int kt = 0; kt < nk; ++kt) {
-      f8_wait_steps<LPS, NS - 2>(min(NS - 2, nk - 1 - kt));
-      f8_barrier();
-      if (kt + NS - 1 < nk) issue((kt + NS - 1) % NS, kb0 + kt + NS - 1);
-      const char* st = lds + (kt % NS) * STAGE;
-      const char* sc = st + A_BYTES + B_BYTES;
-      const float swg = *reinterpret_cast<const float*>(sc + wave * 256 + 128);
-      const float swu = GU ? *reinterpret_cast<const float*>(sc + wave * 256 + 132) : swg;
-      frag_bf16 wf[TN];
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < TN; ++j) wf[j] = widen(lds_frag(st + A_BYTES + (wn * TN + j) * 2048, lane));
+      for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if constexpr (!EXACT) {
+      // Pinned schedule.  A step is TM x TN slots, row tile by row tile.  Slot m issues one
+      // matrix instruction and, while it runs, the four multiply-adds of slot m - 2, whose
+      // result has arrived by then; the fragments and scale of the next row tile are read
+      // during the present one.  The barrier that hands a stage back sits before the last row
+      // tile, whose operands every wave then holds in registers: that tile's matrix
+      // instructions cover the barrier, the reads of the next step's weights (each fragment
+      // right after its last use) and the first loads into the released stage; the remaining
+      // loads go out one per slot at the top of the next step.
+      static_assert(TM >= 2 && TM % 2 == 0 && SLOTS % 4 == 0, "fragment and result buffers alternate");
+      i32x8 wf[TN], af[2];
+      f32x4 p[4];
+      float sg[2] = {0.f, 0.f}, su[2] = {0.f, 0.f}, swg, swu;
+      p[2] = p[3] = f32x4{0.f, 0.f, 0.f, 0.f};  // the first step's slots 0 and 1 add nothing
+      auto madd = [&](int m) __attribute__((always_inline)) {
+        const int i = m / TN, j = m % TN;
+        const float sc = GU && j >= FT ? su[i & 1] : sg[i & 1];
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const frag_bf16 af = widen(lds_frag(st + (wm * TM + i) * 2048, lane));
-        const float s = row_scale(sc, i);
-        const float sg = s * swg, su = s * swu;
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[m & 3][e], sc, acc[i][j][e]);
+      };
+      auto read_af = [&](const char* st, int i, int half) __attribute__((always_inline)) {
+        lds_half(st + (wm * TM + i) * 2048, lane, half, af[i & 1]);
+      };
+      auto read_wf = [&](const char* st, int j) __attribute__((always_inline)) {
+        lds_half(st + A_BYTES + (wn * TN + j) * 2048, lane, 0, wf[j]);
+        lds_half(st + A_BYTES + (wn * TN + j) * 2048, lane, 1, wf[j]);
+      };
+      auto scales_of = [&](float s, int slot) __attribute__((always_inline)) {
+        sg[slot] = s * swg;
+        if constexpr (GU) su[slot] = s * swu;
+      };
+      // Slots of row tile i of a step (stage st); nst: the next step's stage (read in the last
+      // tile); loads l0 .. l1 - 1 of step lkb into stage lbuf go out Q per slot from the top.
+      auto row_tile = [&](int i, const char* st, const char* nst, int lbuf, int lkb, int l0, int l1)
+          __attribute__((always_inline)) {
+        const bool last = i == TM - 1;
+        const char* rst = last ? nst : st;
+        const int ri = last ? 0 : i + 1;
+        float s_next = 0.f, g_next = 0.f, u_next = 0.f;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-          const f32x4 p = mfma_widened(wf[j], af);
-          const float sj = j < FT ? sg : su;
+          const int m = i * TN + j;
+          p[m & 3] = mfma_fp8(wf[j], af[i & 1]);
+          madd((m + SLOTS - 2) % SLOTS);
+          if (last) read_wf(nst, j);
+          if (j == 0) {
+            s_next = row_scale(rst + A_BYTES + B_BYTES, ri);
+            read_af(rst, ri, 0);
+          }
+          if (j == 1) read_af(rst, ri, 1);
+          if (last && j == TN - 1) {
+            const float* w2 = reinterpret_cast<const float*>(nst + A_BYTES + B_BYTES + wave * 256 + 128);
+            g_next = w2[0];
+            if constexpr (GU) u_next = w2[1];
+          }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sj, acc[i][j][e]);
+          for (int q = 0; q < Q; ++q)
+            if (l0 + j * Q + q < l1) issue_one(lbuf, lkb, l0 + j * Q + q);
+          __builtin_amdgcn_sched_barrier(0);
         }
+        if (last) {
+          swg = g_next;
+          swu = u_next;
+        }
+        scales_of(s_next, ri & 1);
+      };
+      {
+        const char* st = lds;
+        const float* w2 = reinterpret_cast<const float*>(st + A_BYTES + B_BYTES + wave * 256 + 128);
+        swg = w2[0];
+        swu = GU ? w2[1] : 0.f;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) read_wf(st, j);
+        read_af(st, 0, 0);
+        read_af(st, 0, 1);
+        scales_of(row_scale(st + A_BYTES + B_BYTES, 0), 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      for (int kt = 0; kt < nk; ++kt) {
+        const int now = kt % NS, nxt = (kt + 1) % NS;
+        const char* st = lds + now * STAGE;
+        const char* nst = lds + nxt * STAGE;
+        // The rest of step kt + NS - 1's loads (its first HALF went out in the last row tile of
+        // the step before).
+#pragma unroll
+        for (int i = 0; i < TM - 1; ++i)
+          row_tile(i, st, nst, (kt + NS - 1) % NS, kb0 + kt + NS - 1, HALF + i * TN * Q, LPS);
+        static_assert(HALF + (TM - 1) * TN * Q >= LPS, "a step's slots hold its loads");
+        // Every wave holds the last row tile's operands (lgkmcnt 0) and step kt + 1 has landed.
+        // (After the last step the reads below fetch fragments that are never used.)
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        wait_vmcnt<(NS - 2) * LPS>();
+        f8_barrier();
+        row_tile(TM - 1, st, nst, now, kb0 + kt + NS, 0, HALF);
+      }
+      // The last two slots' multiply-adds; sg / su of the last row tile are still in place.
+      madd(SLOTS - 2);
+      madd(SLOTS - 1);
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+    } else {
+      for (int kt = 0; kt < nk; ++kt) {
+        if (kt) {
+          wait_vmcnt<(NS - 2) * LPS>();
+          f8_barrier();
+        }
+        issue((kt + NS - 1) % NS, kb0 + kt + NS - 1);
+        const char* st = lds + (kt % NS) * STAGE;
+        const char* sc = st + A_BYTES + B_BYTES;
+        const float swg = *reinterpret_cast<const float*>(sc + wave * 256 + 128);
+        const float swu = GU ? *reinterpret_cast<const float*>(sc + wave * 256 + 132) : swg;
+        frag_bf16 wf[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) wf[j] = widen(lds_frag(st + A_BYTES + (wn * TN + j) * 2048, lane));
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const frag_bf16 af = widen(lds_frag(st + (wm * TM + i) * 2048, lane));
+          const float s = row_scale(sc, i);
+          const float sg = s * swg, su = s * swu;
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            const f32x4 p = mfma_widened(wf[j], af);
+            const float sj = j < FT ? sg : su;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sj, acc[i][j][e]);
+          }
+        }
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+      }
+    }
+    // The ring is free once every wave's loads have landed and its reads are done: the next
+    // tile's first loads go out ahead of this tile's stores.  Loads and stores complete in
+    // order, so the wait at the end counts the stores behind them, a fixed number (rows past
+    // the tile's are dropped by the buffer bounds, not skipped).
+    wait_vmcnt<0>();
+    f8_barrier();
+    if (more) {
+      aim(nxt_place);
+      first_loads();
+    }
+    int stores = 0;  // known when inlined; -1: not fixed
+    const int lane = fresh(), ln = lane & 15, lg = lane >> 4;
+    char* const stg = lds + NS * STAGE + wave * (16 * PITCH);
+    if constexpr (GU) {
+      // h = SiLU(gate) * up, then e4m3 with one scale per row and 128 features: the rows'
+      // largest magnitudes over this wave's features, then over the waves of a row.
+      float* red = reinterpret_cast<float*>(lds + NS * STAGE);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        float mx = 0.f;
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = silu_mul(acc[i][j][e], acc[i][j + FT][e]);
+            acc[i][j][e] = v;
+            mx = fmaxf(mx, fabsf(v));
+          }
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        if (lg == 0) red[wn * BM + (wm * TM + i) * 16 + ln] = mx;
       }
       __builtin_amdgcn_s_waitcnt(0xc07f);
-    }
-  }
-
-  if constexpr (GU) {
-    // h = SiLU(gate) * up, then e4m3 with one scale per row and 128 features: the rows'
-    // largest magnitudes over this wave's features, then over the waves of a row.
-    float* red = reinterpret_cast<float*>(lds);
-    f8_barrier();  // every wave has read its last fragments (lgkmcnt 0 above)
+      f8_barrier();
+      float top[TM];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      float mx = 0.f;
+      for (int i = 0; i < TM; ++i) {
+        top[i] = kAmaxMin;
 #pragma unroll
-      for (int j = 0; j < FT; ++j)
+        for (int v = 0; v < WN; ++v) top[i] = fmaxf(top[i], red[v * BM + (wm * TM + i) * 16 + ln]);
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+      f8_barrier();  // the staging area changes hands
+      const __amdgpu_buffer_rsrc_t hr =
+          make_rsrc(static_cast<uint8_t*>(g.out) + (size_t)cur.start * g.N, (uint32_t)cur.count * (uint32_t)g.N);
+      const __amdgpu_buffer_rsrc_t sr =
+          make_rsrc(g.hs + (size_t)(cur.f0 / 128) * g.hs_ld + cur.start, (uint32_t)cur.count * 4u);
+      static_assert(TM % 4 == 0, "four row tiles' scales per store");
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = silu_mul(acc[i][j][e], acc[i][j + FT][e]);
-          acc[i][j][e] = v;
-          mx = fmaxf(mx, fabsf(v));
+      for (int i = 0; i < TM; i += 4) {
+        // Lane group q stores the scales of row tile i + q (the first wave column's lanes).
+        const float t4 = lg == 0 ? top[i] : lg == 1 ? top[i + 1] : lg == 2 ? top[i + 2] : top[i + 3];
+        const uint32_t r = (uint32_t)((wm * TM + i + lg) * 16 + ln);
+        buf_st4(sr, wn == 0 ? r * 4u : kNoRow, __float_as_uint(t4 / kE4M3Max));
+      }
+      constexpr int HB = 16 * FT;  // bytes of a row: two 16-byte chunks (FT == 2)
+      static_assert(FT == 2 && TM % 2 == 0, "two row tiles per store");
+#pragma unroll
+      for (int i = 0; i < TM; i += 2) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float inv = kE4M3Max * (1.0f / top[i + q]);
+#pragma unroll
+          for (int j = 0; j < FT; ++j)
+            *reinterpret_cast<uint32_t*>(stg + (q * 16 + ln) * (HB + 4) + j * 16 + lg * 4) =
+                pack_fp8x4(acc[i + q][j][0] * inv, acc[i + q][j][1] * inv, acc[i + q][j][2] * inv,
+                           acc[i + q][j][3] * inv);
         }
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      if (lg == 0) red[wn * BM + (wm * TM + i) * 16 + ln] = mx;
-    }
-    __syncthreads();
-    const int blk = f0 / 128;
+        __builtin_amdgcn_wave_barrier();
+        const int rr = lane >> 1, c = lane & 1;
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(stg + rr * (HB + 4) + c * 16);
+        const u32x4 v{from[0], from[1], from[2], from[3]};
+        const uint32_t r = (uint32_t)((wm * TM + i) * 16 + rr);
+        const int n = cur.f0 + wn * HB + c * 16;  // N is a multiple of 16
+        buf_st16(hr, n < g.N ? r * (uint32_t)g.N + (uint32_t)n : kNoRow, v);
+        __builtin_amdgcn_wave_barrier();
+      }
+      stores = TM / 4 + TM / 2;
+    } else {
+      constexpr int CPR = 2 * TN, RPI = 64 / CPR;  // 16-byte chunks per staged row, rows per store
+      const bool split = MODE == F8_LINEAR && gridDim.y > 1;
+      const bool whole = MODE == F8_DOWN
+                             ? !g.out_f32
+                             : !g.out_f32 && !split && cur.f0 + FN <= g.N && g.ldo % 8 == 0 && ((uintptr_t)g.out & 15) == 0;
+      if (whole) {
+        // Rows through LDS: a lane's four features are 8 bytes of 16 different rows, the
+        // stores below whole runs of 32 TN bytes per row.  Projection: bf16.  Experts: fp16
+        // with a power of two per row and 64 columns (11 significant bits at the range of
+        // fp32; bf16 here would show beside the rounding of the sum).
+        const uint32_t rowb = (uint32_t)g.ldo * 2u;
+        const __amdgpu_buffer_rsrc_t yr =
+            make_rsrc(static_cast<char*>(g.out) + (size_t)cur.start * rowb, (uint32_t)(cur.count - 1) * rowb + (uint32_t)g.N * 2u);
+        uint32_t ex[TM];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int r = (wm * TM + i) * 16 + ln;
-      float mx = kAmaxMin;
+        for (int i = 0; i < TM; ++i) {
+          float up = 1.f;
+          if constexpr (MODE == F8_DOWN) {
+            float mx = 0.f;
 #pragma unroll
-      for (int v = 0; v < WN; ++v) mx = fmaxf(mx, red[v * BM + r]);
-      const float inv = kE4M3Max * (1.0f / mx);
-      if (r >= count) continue;
-      if (wn == 0 && lg == 0) g.hs[(size_t)blk * g.hs_ld + start + r] = mx / kE4M3Max;
+            for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int j = 0; j < FT; ++j) {
-        const int n = f0 + wn * 16 * FT + 16 * j + 4 * lg;  // N is a multiple of 16
-        if (n < g.N)
-          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(g.out) + (size_t)(start + r) * g.N + n) =
-              pack_fp8x4(acc[i][j][0] * inv, acc[i][j][1] * inv, acc[i][j][2] * inv, acc[i][j][3] * inv);
+              for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(acc[i][j][e]));
+            mx = fmaxf(mx, __shfl_xor(mx, 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            ex[i] = max(__float_as_uint(mx) >> 23, 15u);        // exponent field of the largest
+            up = __uint_as_float((268u - ex[i]) << 23);         // brings it to [2^14, 2^15)
+          }
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            u32x2 v;
+            if constexpr (MODE == F8_DOWN)
+              v = u32x2{f2h(acc[i][j][0] * up) | f2h(acc[i][j][1] * up) << 16,
+                        f2h(acc[i][j][2] * up) | f2h(acc[i][j][3] * up) << 16};
+            else
+              v = u32x2{pack_bf2(acc[i][j][0], acc[i][j][1]), pack_bf2(acc[i][j][2], acc[i][j][3])};
+            *reinterpret_cast<u32x2*>(stg + ln * PITCH + j * 32 + lg * 8) = v;
+          }
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int q = 0; q < 16 / RPI; ++q) {
+            const int rr = q * RPI + lane / CPR;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(stg + rr * PITCH + (lane % CPR) * 16);
+            const uint32_t r = (uint32_t)((wm * TM + i) * 16 + rr);
+            const int n = cur.f0 + wn * 16 * TN + (lane % CPR) * 8;
+            buf_st16(yr, n < g.N && (int)r < cur.count ? r * rowb + (uint32_t)n * 2u : kNoRow, v);
+          }
+          __builtin_amdgcn_wave_barrier();
+        }
+        if constexpr (MODE == F8_DOWN) {
+          const __amdgpu_buffer_rsrc_t er = make_rsrc(
+              g.yexp + (size_t)(cur.f0 / 64 + wn) * g.hs_ld + cur.start, cur.f0 + wn * 64 < g.N ? (uint32_t)cur.count : 0u);
+#pragma unroll
+          for (int i = 0; i < TM; i += 4) {
+            const uint32_t e4 = lg == 0 ? ex[i] : lg == 1 ? ex[i + 1] : lg == 2 ? ex[i + 2] : ex[i + 3];
+            buf_st1(er, (uint32_t)((wm * TM + i + lg) * 16 + ln), e4);
+          }
+        }
+        stores = TM * (16 / RPI) + (MODE == F8_DOWN ? TM / 4 : 0);
+      } else {
+        stores = -1;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const int r = (wm * TM + i) * 16 + ln;
+          if (r >= cur.count) continue;
+          const size_t row = (size_t)(cur.start + r);
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            const int n = cur.f0 + (wn * TN + j) * 16 + 4 * lg;
+            if (n >= g.N) continue;
+            if (split) {
+              float* p = g.part + ((size_t)blockIdx.y * g.M + row) * (size_t)g.N + n;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (n + e < g.N) p[e] = acc[i][j][e];
+            } else {
+              f8_store4(g, row, n, acc[i][j]);
+            }
+          }
+        }
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int r = (wm * TM + i) * 16 + ln;
-      if (r >= count) continue;
-      const size_t row = MODE == F8_DOWN ? (size_t)g.perm[start + r] : (size_t)(start + r);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int n = f0 + (wn * TN + j) * 16 + 4 * lg;
-        if (n >= g.N) continue;
-        if (MODE == F8_LINEAR && gridDim.y > 1) {
-          float* p = g.part + ((size_t)blockIdx.y * g.M + row) * (size_t)g.N + n;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < g.N) p[e] = acc[i][j][e];
-        } else {
-          f8_store4(g, row, n, acc[i][j]);
-        }
-      }
-    }
+    if (!more) break;
+    constexpr int CPRW = 2 * TN;
+    constexpr int FIXED = GU ? TM / 4 + TM / 2 : TM * (16 * CPRW / 64) + (MODE == F8_DOWN ? TM / 4 : 0);
+    static_assert(AHEAD + FIXED < 64, "vmcnt range");
+    if (stores == FIXED) wait_vmcnt<AHEAD + FIXED>();
+    else wait_vmcnt<0>();
+    lin += (int)gridDim.x;
+    cur = nxt_place;
   }
 }
 
@@ -1177,7 +1356,8 @@ struct PrepArgs {
   const int32_t* ids;
   int pairs, E, first, bm;
   int* hdr;    // [0] tiles, then 4 words per tile
-  int* perm;
+  int* perm;   // pair at each sorted position
+  int* place;  // sorted position of each pair, -1 for other ranks' pairs
   QuantArgs q;
 };
 
@@ -1237,20 +1417,24 @@ __global__ __launch_bounds__(kPrepThreads) void experts_prep_kernel(PrepArgs a) 
     const int p = p0 + tid;
     if (p < a.pairs) {
       const int e = local_expert(a.ids[p], a.first, a.E);
-      if (e >= 0) a.perm[atomicAdd(&off[e], 1)] = p;
+      const int at = e >= 0 ? atomicAdd(&off[e], 1) : -1;
+      a.place[p] = at;
+      if (e >= 0) a.perm[at] = p;
     }
     __syncthreads();
   }
 }
 
-// out[t] = sum_j weights[t, j] y[t * topk + j] over the local experts, in fp32.
+// out[t] = sum_j weights[t, j] y[place of (t, j)] over the local experts, in fp32.
 struct CombineArgs {
-  const void* y;
+  const void* y;         // fp32, or fp16 with exponents
   int y_f32;
-  const int32_t* ids;
+  const uint8_t* yexp;
+  int P;
+  const int* place;
   const float* weights;
   void* out;
-  int T, H, E, first, topk, out_f32;
+  int T, H, topk, out_f32;
 };
 
 __global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
@@ -1260,11 +1444,22 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
     const int t = (int)(i / per), c = (int)(i - (int64_t)t * per) * 8;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < a.topk; ++j) {
-      const int64_t p = (int64_t)t * a.topk + j;
-      if (local_expert(a.ids[p], a.first, a.E) < 0) continue;
-      const float w = a.weights[p];
+      const int at = a.place[(size_t)t * a.topk + j];
+      if (at < 0) continue;
+      float w = a.weights[(size_t)t * a.topk + j];
       float v[8];
-      load8(a.y, (size_t)p * a.H + c, !a.y_f32, v);
+      if (a.y_f32) {
+        load8(a.y, (size_t)at * a.H + c, 0, v);
+      } else {
+        const u32x4 u = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.y) + (size_t)at * a.H + c));
+        const float down = __uint_as_float((uint32_t)(a.yexp[(size_t)(c / 64) * a.P + at] - 14) << 23);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[2 * q] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[q] & 0xffffu)) * down;
+          v[2 * q + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[q] >> 16)) * down;
+        }
+      }
 #pragma unroll
       for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
     }
@@ -1304,7 +1499,9 @@ int launch_f8(const F8Plan& p, const F8Args& a, int max_tiles, hipStream_t s) {
   F8Args g = a;
   g.tiles_n = (a.N + fn - 1) / fn;
   g.tiles_m = max_tiles;
-  const dim3 grid((unsigned)(g.tiles_n * max_tiles), (unsigned)p.ksplit);
+  // One workgroup per compute unit (two of the small tiles), each taking every so-manieth tile.
+  const int resident = (p.bm * p.bn <= 128 * 128 ? 2 : 1) * kCUs, tiles = g.tiles_n * max_tiles;
+  const dim3 grid((unsigned)(tiles < resident ? tiles : resident), (unsigned)p.ksplit);
 #define SMLP_F8(BM_, BN_, WM_, WN_, NS_)                                                               \
   if (p.bm == BM_ && p.bn == BN_) {                                                                    \
     if (p.exact)                                                                                       \
@@ -1316,7 +1513,7 @@ int launch_f8(const F8Plan& p, const F8Args& a, int max_tiles, hipStream_t s) {
     return (int)hipGetLastError();                                                                     \
   }
   SMLP_F8(64, 256, 1, 4, 3) SMLP_F8(256, 256, 2, 4, 2)
-  if constexpr (MODE != F8_GATE_UP) { SMLP_F8(64, 64, 2, 2, 4) SMLP_F8(128, 128, 2, 2, 3) }
+  if constexpr (MODE == F8_LINEAR) { SMLP_F8(64, 64, 2, 2, 4) SMLP_F8(128, 128, 2, 2, 2) }
 #undef SMLP_F8
   return (int)hipErrorInvalidConfiguration;
 }
@@ -1462,6 +1659,7 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
   pa.bm = p.gu.bm;
   pa.hdr = hdr;
   pa.perm = perm;
+  pa.place = reinterpret_cast<int*>(base + p.place_off);
   pa.q.x = c.x;
   pa.q.rows = p.T;
   pa.q.cols = (int)p.H;
@@ -1526,6 +1724,8 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
   d.out = y;
   d.ldo = (int)p.H;
   d.out_f32 = p.y_f32;
+  d.hs_ld = (int)p.P;
+  d.yexp = reinterpret_cast<uint8_t*>(base + p.yexp_off);
   d.kslice = (int)IB;
   rc = short_k ? launch_f8_down(p.dn, d, h32, (int)p.max_tiles, s) : launch_f8<F8_DOWN>(p.dn, d, (int)p.max_tiles, s);
   if (rc) return rc;
@@ -1533,13 +1733,13 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
   CombineArgs ca{};
   ca.y = y;
   ca.y_f32 = p.y_f32;
-  ca.ids = c.ids;
+  ca.yexp = reinterpret_cast<const uint8_t*>(base + p.yexp_off);
+  ca.P = (int)p.P;
+  ca.place = reinterpret_cast<const int*>(base + p.place_off);
   ca.weights = c.weights;
   ca.out = c.out;
   ca.T = (int)p.T;
   ca.H = (int)p.H;
-  ca.E = (int)p.E;
-  ca.first = (int)c.first;
   ca.topk = (int)p.topk;
   ca.out_f32 = c.out_f32;
   const int64_t n = (p.T * (p.H / 8) + 255) / 256;

@@ -140,6 +140,7 @@ int launch_bf16_to_f16(const void* src, int64_t ld_src, int64_t rows, int64_t co
 int launch_route(const void* logits, int bf16, int64_t T, int64_t E, int64_t ldl, const float* bias,
                  const smlp_route& r, int32_t* ids, float* weights, hipStream_t s);
 
+constexpr int kCUs = 256;  // compute units the grids are sized for
 // Limits of the short-K down kernel (16-row weight tiles per workgroup) and of the kernels
 // for one token (blocks of 128 in H; blocks of 128 in I over all pairs).
 constexpr int kDownRun = 496, kTokenBlocks = 64, kTokenPairBlocks = 64;
@@ -175,8 +176,8 @@ struct ExpertsPlan {
   int64_t max_tiles;    // row tiles that any routing can need
   F8Plan gu, dn;
   int token;            // one token: two launches without a sort
-  int y_f32;            // rows of y held in fp32 (1) or bf16 (0)
-  size_t hdr_off, perm_off, x8_off, xs_off, h8_off, hs_off, h32_off, y_off, workspace_bytes;
+  int y_f32;            // rows of y held in fp32 (1) or fp16 with exponents (0)
+  size_t hdr_off, perm_off, place_off, yexp_off, x8_off, xs_off, h8_off, hs_off, h32_off, y_off, workspace_bytes;
 };
 struct ExpertsCall {
   const void* x;

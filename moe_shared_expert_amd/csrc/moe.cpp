@@ -10,7 +10,6 @@
 
 namespace {
 
-constexpr int64_t kCUs = 256;  // compute units the grids are sized for
 constexpr int64_t kLimit = (int64_t)1 << 31;
 
 int fail(int status, const char* fmt, ...) {
@@ -142,7 +141,7 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
       // over the (tile, run of weight tiles) pairs, at least four weight tiles each.
       p.dn.kind = smlp::F8_KIND_DOWN;
       const int64_t ht = (H + 15) / 16, tiles = active ? p.P / p.dn.bm + active : 1;
-      const int64_t runs = (4 * kCUs + tiles - 1) / tiles, run = (ht + runs - 1) / runs;
+      const int64_t runs = (4 * smlp::kCUs + tiles - 1) / tiles, run = (ht + runs - 1) / runs;
       p.dn.run = (int)(run < 4 ? 4 : run > smlp::kDownRun ? smlp::kDownRun : (run + 3) / 4 * 4);
     }
   } else {
@@ -163,6 +162,8 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
   };
   p.hdr_off = take((size_t)(4 + 4 * p.max_tiles) * 4);
   p.perm_off = take((size_t)p.P * 4);
+  p.place_off = take((size_t)p.P * 4);
+  p.yexp_off = take(p.y_f32 ? 0 : (size_t)p.P * (size_t)((H + 63) / 64));
   p.x8_off = take((size_t)(T * H));
   p.xs_off = take((size_t)(T * HB) * 4);
   p.h8_off = take((size_t)(p.P * I));
