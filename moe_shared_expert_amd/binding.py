@@ -460,8 +460,24 @@ def shared_mlp_forward_rank(x, w_gate_up, w_down, out, tp: int, rank: int, works
 
 
 # The routed half of the layer (include/smlp.h): routing, the 8-bit block-scaled product, the
-# routed experts.  Decode calls take a few microseconds on the GPU, so the marshalling here is
-# kept short: sizes and options that repeat are looked up, never tensors.
+# routed experts.  Decode calls take a few microseconds on the GPU, less than their marshalling
+# in Python: the allocating forms (route, linear_fp8, experts_fp8) go through the compiled
+# module _calls, which takes the same steps on torch's C++ tensors.
+_calls = None
+
+
+def _load_calls():
+    global _calls
+    lib()
+    path = os.path.join(_HERE, "_calls.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with `python -m moe_shared_expert_amd.build` "
+                           "(no fallback exists)")
+    from . import _calls as module
+    module.set_check(_check)
+    _calls = module
+    return module
+
 
 FP8 = torch.float8_e4m3fn
 ROUTE_SCORES = {"sigmoid": 0, "softmax": 1}
@@ -531,11 +547,11 @@ def shared_mlp_route(logits, ids, weights, score="sigmoid", bias=None, groups=1,
 def route(logits, topk: int, score="sigmoid", bias=None, groups=1, top_groups=None, group_top=1, renormalize=True,
           scale=1.0, stream=None):
     """Allocating form of shared_mlp_route; returns ids, weights."""
-    T, dev = logits.shape[0], logits.device
-    ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
-    shared_mlp_route(logits, ids, weights, score, bias, groups, top_groups, group_top, renormalize, scale, stream)
-    return ids, weights
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score {score!r} is not one of {sorted(ROUTE_SCORES)}")
+    return (_calls or _load_calls()).route(logits, topk, ROUTE_SCORES[score], bias, groups,
+                                           groups if top_groups is None else top_groups, group_top, renormalize, scale,
+                                           None if stream is None else _queue(stream, 0))
 
 
 def shared_mlp_quant_fp8(x, q, scales, block_rows=1, stream=None):
@@ -601,8 +617,8 @@ def shared_mlp_linear_fp8(x, w, w_scales, y, x_scales=None, workspace=None, stre
 
 def linear_fp8(x, w, w_scales, x_scales=None, out_fp32=False, workspace=None, stream=None):
     """Allocating form of shared_mlp_linear_fp8."""
-    y = torch.empty((x.shape[0], w.shape[0]), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=x.device)
-    return shared_mlp_linear_fp8(x, w, w_scales, y, x_scales, workspace, stream)
+    return (_calls or _load_calls()).linear_fp8(x, w, w_scales, x_scales, out_fp32, workspace,
+                                                None if stream is None else _queue(stream, 0))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -642,9 +658,9 @@ def shared_mlp_experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down
 def experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert=0, partial_fp32=False,
                 workspace=None, stream=None):
     """Allocating form of shared_mlp_experts_fp8."""
-    out = torch.empty(x.shape, dtype=torch.float32 if partial_fp32 else torch.bfloat16, device=x.device)
-    return shared_mlp_experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, out, first_expert, workspace,
-                                  stream)
+    return (_calls or _load_calls()).experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert,
+                                                 partial_fp32, workspace,
+                                                 None if stream is None else _queue(stream, 0))
 
 
 # Measurement kernels (include/smlp_ceilings.h): launch them, time them on the caller's side.

@@ -1,9 +1,9 @@
-"""Build libsmlp.so in-tree with hipcc for gfx950.
+"""Build libsmlp.so in-tree with hipcc for gfx950, and the Python module of the short calls.
 
     python -m moe_shared_expert_amd.build
 
 Every call recompiles all sources (object files go to ``_build/`` next to this file,
-the library to ``libsmlp.so`` next to this file).
+the library to ``libsmlp.so`` and the module to ``_calls.so`` next to this file).
 """
 from __future__ import annotations
 
@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsmlp.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 SOURCES = ["api.cpp", "layout.cpp", "skinny.hip", "gemm.hip", "aux.hip", "latent.hip", "ceilings.hip",
            "noalloc.hip", "moe.cpp", "route.hip", "fp8.hip"]
@@ -46,18 +48,49 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_calls() -> str:
+    """torch_calls.cpp against torch's headers (host code only)."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "torch_calls.o")
+    cmd = [shutil.which("g++") or "g++", "-c", os.path.join(CSRC, "torch_calls.cpp"), "-o", obj, "-O2", "-fPIC",
+           "-std=c++17", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"], "-Wall"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, LIB, "-L" + lib, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), 8)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(_compile, SOURCES))
+        calls_obj = calls.result()
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), "-shared", "-fPIC", "-o", tmp, *objs, "--offload-arch=" + ARCH]
+    cmd = [hipcc(), "-shared", "-fPIC", "-o", tmp, *objs, "--offload-arch=" + ARCH, "-Wl,-soname,libsmlp.so"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_calls(calls_obj)
     if verbose:
-        print("built", LIB)
+        print("built", LIB, "and", CALLS)
     return LIB
 
 

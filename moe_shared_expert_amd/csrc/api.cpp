@@ -889,11 +889,6 @@ int run(Stage stage, const void* x, const void* wgu, const void* wd, void* out, 
 
 }  // namespace
 
-int smlp::set_status(int status, const char* detail) {
-  g_last_error = detail;
-  return status;
-}
-
 namespace smlp {
 // Counter slot of a stream (one-launch decode layer, in-launch K-split reductions):
 // launches on one stream run one after another and share a slot; each stream gets its

@@ -450,6 +450,155 @@ __global__ __launch_bounds__(256) void f8_down_kernel(F8Args g, const float* h, 
   wait_vmcnt<0>();
 }
 
+// Projection of up to 16 bf16 rows in one launch: a lane loads the 32 elements of x that it
+// holds of a fragment, finds the group's largest magnitude with the three other lanes of its
+// row, and has both its fragment and its scale (of the column it holds results for) in
+// registers.  A workgroup owns NT tiles of 16 weight rows; its 8 waves take the K blocks in
+// turn, D blocks of loads in flight, and their sums are added in wave order.  The work on x
+// (about 200 instructions a block, for every workgroup anew) bounds a workgroup, so with few
+// weight rows K is split over workgroups too (gridDim.y); the last one to arrive at a counter
+// adds the slices in order.
+struct NarrowArgs {
+  const void* x;   // [M, K] bf16
+  const uint8_t* w;
+  const float* ws;
+  F8Args g;        // M, K, KB, N, nblk, out, ldo, out_f32, w_bytes; kslice, part: K split
+  uint32_t* arrived;  // one counter per blockIdx.x, 16 words apart, zero between launches
+};
+
+template <int NT, int D>
+__global__ __launch_bounds__(512, 2) void f8_narrow_kernel(NarrowArgs a) {
+  constexpr int WAVES = 8;
+  __shared__ f32x4 red[WAVES][NT][64];
+  __shared__ int last;
+  const F8Args& g = a.g;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ln = lane & 15, lg = lane >> 4;
+  const int K = g.K, n0 = blockIdx.x * (16 * NT);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)g.M * (uint32_t)K * 2u), wr = make_rsrc(a.w, g.w_bytes);
+  const uint32_t xo = ln < g.M ? ((uint32_t)ln * (uint32_t)K + lg * 16) * 2u : kNoRow;
+  uint32_t wo[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int n = n0 + 16 * t + ln;
+    wo[t] = n < g.N ? (uint32_t)n * (uint32_t)K + lg * 16 : kNoRow;
+  }
+  struct Block {
+    u32x4 x[4], w[NT][2];
+    float s;
+  };
+  Block q[D];
+  const float* ws = a.ws + (size_t)min(n0 / 128, g.nblk - 1) * g.KB;
+  const int kb0 = blockIdx.y * g.kslice, kb1 = min(g.KB, kb0 + g.kslice);
+  auto load = [&](Block& b, int i) __attribute__((always_inline)) {
+    const int kb = kb0 + i * WAVES + wave, k = kb * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = kb < kb1 && k + 64 * h + lg * 16 < K;
+      const uint32_t ko = in ? (uint32_t)(k + 64 * h) : kNoChunk;
+      const uint32_t kx = in ? 2u * (uint32_t)(k + 64 * h) : kNoChunk;
+      b.x[2 * h] = buf_ld(xr, xo + kx);
+      b.x[2 * h + 1] = buf_ld(xr, xo + kx + (in ? 16u : 0u));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) b.w[t][h] = buf_ld_nt(wr, wo[t] + ko);
+    }
+    b.s = ws[min(kb, g.KB - 1)];
+  };
+  f32x4 acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto use = [&](const Block& b) __attribute__((always_inline)) {
+    float v[32], mx = kAmaxMin;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[8 * c + 2 * i] = bf_lo(b.x[c][i]);
+        v[8 * c + 2 * i + 1] = bf_hi(b.x[c][i]);
+      }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(v[i]));
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float inv = kE4M3Max * (1.0f / mx);
+    i32x8 af;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      af[i] = (int)pack_fp8x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    const frag_bf16 fa = widen(af);
+    const float s = (mx / kE4M3Max) * b.s;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      i32x8 wf;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        wf[i] = (int)b.w[t][0][i];
+        wf[4 + i] = (int)b.w[t][1][i];
+      }
+      const f32x4 p = mfma_widened(widen(wf), fa);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[t][j] = fmaf(p[j], s, acc[t][j]);
+    }
+  };
+  const int nst = (kb1 - kb0 + WAVES - 1) / WAVES;  // blocks past the slice are zeros
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(q[d], d);
+  int i0 = 0;
+  for (; i0 + D < nst; i0 += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      use(q[d]);
+      load(q[d], i0 + D + d);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (i0 + d < nst) use(q[d]);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) red[wave][t][lane] = acc[t];
+  __syncthreads();
+  f32x4 sum{0.f, 0.f, 0.f, 0.f};
+  if (wave < NT) {
+    sum = red[0][wave][lane];
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) sum += red[v][wave][lane];
+  }
+  const int slices = gridDim.y;
+  if (slices > 1) {
+    // Partial sums, agent-coherent: [slice][column of workgroups][tile][lane][4].
+    const size_t col = ((size_t)blockIdx.x * NT + wave) * 256 + lane * 4, step = (size_t)gridDim.x * NT * 256;
+    if (wave < NT) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        __hip_atomic_store(g.part + blockIdx.y * step + col + j, sum[j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    wait_vmcnt<0>();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint32_t* c = a.arrived + 16 * blockIdx.x;
+      const bool l = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)slices - 1;
+      if (l) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = l;
+    }
+    __syncthreads();
+    if (!last || wave >= NT) return;
+    const __amdgpu_buffer_rsrc_t pr = make_rsrc(g.part, (uint32_t)(slices * step * 4));
+    f32x4 v[kNarrowSlices];
+#pragma unroll
+    for (int q = 0; q < kNarrowSlices; ++q)
+      v[q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                 pr, (int)(q < slices ? (uint32_t)((q * step + col) * 4) : kNoRow), 0, 16));
+    sum = v[0];
+#pragma unroll
+    for (int q = 1; q < kNarrowSlices; ++q) sum += v[q];  // slices past the last are zeros
+  }
+  if (wave >= NT) return;
+  const int n = n0 + 16 * wave + 4 * lg;
+  if (ln < g.M && n < g.N) f8_store4(g, (size_t)ln, n, sum);
+}
+
 // ---- one activation row ----
 // A single row leaves the matrix instructions with one column in sixteen, so these kernels
 // multiply in the vector unit, straight from registers: a 16-byte load per lane covers 8
@@ -1557,6 +1706,32 @@ int launch_row_fp8(const void* x, const float* xs, const void* w, const float* w
   t.out = y;
   t.out_f32 = out_f32;
   hipLaunchKernelGGL((f8_row_kernel<false, 14>), dim3((unsigned)((N + 7) / 8)), dim3(256), 0, s, t);
+  return (int)hipGetLastError();
+}
+
+int launch_narrow_fp8(const F8Plan& p, const void* x, const void* w, const float* ws, void* y, int64_t M, int64_t K,
+                      int64_t N, int64_t ldy, int out_f32, float* part, hipStream_t s) {
+  NarrowArgs a{};
+  a.x = x;
+  a.w = static_cast<const uint8_t*>(w);
+  a.ws = ws;
+  a.g.w_bytes = (uint32_t)(N * K);
+  a.g.K = (int)K;
+  a.g.KB = (int)((K + 127) / 128);
+  a.g.N = (int)N;
+  a.g.nblk = (int)((N + 127) / 128);
+  a.g.M = (int)M;
+  a.g.out = y;
+  a.g.ldo = (int)ldy;
+  a.g.out_f32 = out_f32;
+  const int cols = (int)((N + 16 * p.nt - 1) / (16 * p.nt));
+  a.arrived = p.ksplit > 1 ? reduce_counters(s, cols) : nullptr;
+  const int slices = a.arrived ? p.ksplit : 1;  // no counters left for this stream: no split
+  a.g.kslice = slices > 1 ? p.kslice : a.g.KB;
+  a.g.part = part;
+  const dim3 grid((unsigned)cols, (unsigned)slices);
+  if (p.nt == 1) hipLaunchKernelGGL((f8_narrow_kernel<1, 4>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((f8_narrow_kernel<2, 3>), grid, dim3(512), 0, s, a);
   return (int)hipGetLastError();
 }
 

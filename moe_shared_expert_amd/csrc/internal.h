@@ -10,7 +10,7 @@ namespace smlp {
 
 // Record a status and its detail (shared_mlp_last_error) and return the status (api.cpp);
 // SMLP_OK clears the detail.
-int set_status(int status, const char* detail);
+int set_error(int status, const char* msg);
 
 // One weight-streaming (small-M) stage: out-features in blocks of 16, K split into
 // `ksplit` slices over workgroups and into `waves` slices inside a workgroup.
@@ -144,9 +144,11 @@ constexpr int kCUs = 256;  // compute units the grids are sized for
 // Limits of the short-K down kernel (16-row weight tiles per workgroup) and of the kernels
 // for one token (blocks of 128 in H; blocks of 128 in I over all pairs).
 constexpr int kDownRun = 496, kTokenBlocks = 64, kTokenPairBlocks = 64;
+// Most K slices of the projection of up to 16 rows, and its columns of workgroups then.
+constexpr int kNarrowSlices = 8, kNarrowColumns = 256;
 
 // One 8-bit block-scaled product (fp8.hip).
-enum { F8_KIND_STREAM = 0, F8_KIND_TILE = 1, F8_KIND_DOWN = 2, F8_KIND_ROW = 3 };
+enum { F8_KIND_STREAM = 0, F8_KIND_TILE = 1, F8_KIND_DOWN = 2, F8_KIND_ROW = 3, F8_KIND_NARROW = 4 };
 struct F8Plan {
   int kind;
   int bm;                     // activation rows per tile
@@ -165,6 +167,10 @@ int launch_quant_fp8(const void* x, int bf16, int64_t parts, int64_t rows, int64
 // The product for one row (K <= 128 * kTokenBlocks): x bf16 (xs null) or e4m3 with scales.
 int launch_row_fp8(const void* x, const float* xs, const void* w, const float* ws, void* y, int64_t K, int64_t N,
                    int out_f32, hipStream_t s);
+// The product for up to 16 bf16 rows (M * K < 2^30) in one launch; with a K split `part` holds
+// ksplit x columns of workgroups x nt x 256 fp32 partials.
+int launch_narrow_fp8(const F8Plan& p, const void* x, const void* w, const float* ws, void* y, int64_t M, int64_t K,
+                      int64_t N, int64_t ldy, int out_f32, float* part, hipStream_t s);
 int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t as_row, int64_t as_kb,
                       const void* w, const float* ws, void* y, int64_t M, int64_t K, int64_t N, int64_t ldy,
                       int out_f32, float* part, hipStream_t s);

@@ -18,10 +18,10 @@ int fail(int status, const char* fmt, ...) {
   va_start(ap, fmt);
   std::vsnprintf(buf, sizeof buf, fmt, ap);
   va_end(ap);
-  return smlp::set_status(status, buf);
+  return smlp::set_error(status, buf);
 }
 
-int ok() { return smlp::set_status(SMLP_OK, ""); }
+int ok() { return smlp::set_error(SMLP_OK, ""); }
 
 int hip_status(int rc, const char* what) {
   if (rc == (int)hipSuccess) return SMLP_OK;
@@ -85,10 +85,26 @@ int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, L
     return fail(SMLP_ERR_SHAPE, "M*K, N*K and M*N must be below 2^31");
   LinearF8Plan p{};
   const int64_t KB = blocks128(K);
+  size_t part = 0;
   if (M == 1 && KB <= smlp::kTokenBlocks) {
     p.f = stream_plan(M, KB);
     p.f.kind = smlp::F8_KIND_ROW;  // x is brought to its 8-bit form in each workgroup
     x_fp8 = 1;
+  } else if (M <= 16 && !x_fp8 && M * K < kLimit / 2) {
+    p.f = stream_plan(M, KB);
+    p.f.kind = smlp::F8_KIND_NARROW;
+    p.f.nt = N > 16 * 2 * smlp::kCUs ? 2 : 1;
+    x_fp8 = 1;  // likewise
+    // Up to two workgroups per compute unit, at least one block per wave.
+    const int64_t cols = (N + 16 * p.f.nt - 1) / (16 * p.f.nt);
+    int64_t slices = 2 * smlp::kCUs / cols;
+    if (slices > (KB + 7) / 8) slices = (KB + 7) / 8;
+    if (slices > smlp::kNarrowSlices) slices = smlp::kNarrowSlices;
+    if (slices > 1 && cols <= smlp::kNarrowColumns) {
+      p.f.kslice = (int)((KB + slices - 1) / slices);
+      p.f.ksplit = (int)((KB + p.f.kslice - 1) / p.f.kslice);
+      part = (size_t)p.f.ksplit * (size_t)(cols * p.f.nt) * 256 * 4;
+    }
   } else if (M <= 32) {
     p.f = stream_plan(M, KB);
   } else {
@@ -106,7 +122,8 @@ int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, L
   p.xs_off = off;
   if (!x_fp8) off += round_up((size_t)(M * KB) * 4);
   p.part_off = off;
-  if (p.f.ksplit > 1) off += round_up((size_t)p.f.ksplit * (size_t)(M * N) * 4);
+  if (p.f.kind == smlp::F8_KIND_TILE && p.f.ksplit > 1) part = (size_t)p.f.ksplit * (size_t)(M * N) * 4;
+  off += round_up(part);
   p.workspace_bytes = off;
   *out = p;
   return SMLP_OK;
@@ -294,6 +311,12 @@ int shared_mlp_linear_fp8(const void* x, const float* x_scales, const void* w, c
   (void)hipGetLastError();
   if (p.f.kind == smlp::F8_KIND_ROW) {
     rc = smlp::launch_row_fp8(x, x_scales, w, w_scales, y, K, N, out_fp32, stream);
+    if ((rc = hip_status(rc, "8-bit product launch"))) return rc;
+    return ok();
+  }
+  if (p.f.kind == smlp::F8_KIND_NARROW) {
+    rc = smlp::launch_narrow_fp8(p.f, x, w, w_scales, y, M, K, N, ldy, out_fp32,
+                                 reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_off), stream);
     if ((rc = hip_status(rc, "8-bit product launch"))) return rc;
     return ok();
   }

@@ -11,7 +11,7 @@ static std::string g_detail;
 static int g_launches = 0;
 
 namespace smlp {
-int set_status(int status, const char* detail) {
+int set_error(int status, const char* detail) {
   g_detail = detail;
   return status;
 }
@@ -24,6 +24,10 @@ int launch_quant_fp8(const void*, int, int64_t, int64_t, int64_t, int64_t, int, 
   return ++g_launches, 0;
 }
 int launch_row_fp8(const void*, const float*, const void*, const float*, void*, int64_t, int64_t, int, hipStream_t) {
+  return ++g_launches, 0;
+}
+int launch_narrow_fp8(const F8Plan&, const void*, const void*, const float*, void*, int64_t, int64_t, int64_t, int64_t,
+                      int, float*, hipStream_t) {
   return ++g_launches, 0;
 }
 int launch_linear_fp8(const F8Plan&, const void*, const float*, int64_t, int64_t, const void*, const float*, void*,

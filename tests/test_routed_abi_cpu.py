@@ -124,7 +124,7 @@ def test_quant_refusals(L, kw, status):
     (dict(y=D), ALIAS), (dict(buf=A), ALIAS), (dict(buf=C), ALIAS), (dict(y=W), ALIAS), (dict(xs=E_), ALIAS),
 ])
 def test_linear_refusals(L, kw, status):
-    o = dict(x=A, xs=None, w=C, ws=D, y=E_, M=10, K=256, N=100, ldy=100, f32=0, buf=W, n=1 << 20)
+    o = dict(x=A, xs=None, w=C, ws=D, y=E_, M=40, K=256, N=100, ldy=100, f32=0, buf=W, n=1 << 20)
     o.update(kw)
     assert L.shared_mlp_linear_fp8(*o.values(), None) == status
 
@@ -148,8 +148,10 @@ def test_experts_refusals(L, kw, status):
 
 def test_workspace_sizes(L):
     assert binding.shared_mlp_linear_fp8_workspace_bytes(0, 256, 64, False) == 0
+    # x of up to 16 rows is brought to its 8-bit form inside the product
     assert binding.shared_mlp_linear_fp8_workspace_bytes(1, 7168, 2112, False) == 0
-    for M in (2, 17, 100, 5000):
+    assert binding.shared_mlp_linear_fp8_workspace_bytes(16, 7168, 7168, False) == 0
+    for M in (17, 100, 5000):
         assert binding.shared_mlp_linear_fp8_workspace_bytes(M, 7168, 2112, False) >= M * (7168 + 4 * 56)
     small = binding.shared_mlp_experts_fp8_workspace_bytes(1, 7168, 768, 128, 8)
     big = binding.shared_mlp_experts_fp8_workspace_bytes(8192, 7168, 768, 128, 8)
