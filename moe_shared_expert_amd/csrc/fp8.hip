@@ -1498,42 +1498,47 @@ __global__ __launch_bounds__(256) void quant_blocks_kernel(QuantArgs a, int rows
   if (threadIdx.x == 0) a.s[(rb * KB) + b] = mx / kE4M3Max;
 }
 
-// First launch of the experts: workgroup 0 sorts the pairs (token, choice) by expert and
-// writes the tile list; the others quantise x.  Pairs whose expert is outside
-// [first, first + E) are dropped.
+// First launches of the experts: sort the pairs (token, choice) by expert, write the tile
+// list, and quantise x beside that.  Pairs whose expert is outside [first, first + E) are
+// dropped.  Up to kOneSort pairs one workgroup sorts; above, workgroup b counts its chunk of
+// pairs, and a second launch places them from the counts (65536 pairs: one workgroup took
+// 90 us, most of it waiting for its own loads).
 struct PrepArgs {
   const int32_t* ids;
   int pairs, E, first, bm;
-  int* hdr;    // [0] tiles, then 4 words per tile
-  int* perm;   // pair at each sorted position
-  int* place;  // sorted position of each pair, -1 for other ranks' pairs
+  int* hdr;     // [0] tiles, then 4 words per tile
+  int* perm;    // pair at each sorted position
+  int* place;   // sorted position of each pair, -1 for other ranks' pairs
+  int* counts;  // [chunks][E]
+  int chunk, chunks;
   QuantArgs q;
 };
 
 constexpr int kPrepThreads = 1024;
 
-__global__ __launch_bounds__(kPrepThreads) void experts_prep_kernel(PrepArgs a) {
-  if (blockIdx.x > 0) {
-    const int KB = (a.q.cols + 127) / 128;
-    const int64_t groups = a.q.rows * KB;
-    constexpr int PER = kPrepThreads / 16;
-    const int64_t step = (int64_t)(gridDim.x - 1) * PER;
-    for (int64_t g = (int64_t)(blockIdx.x - 1) * PER; g < groups; g += step)
-      quant_group(a.q, g + (threadIdx.x >> 4), KB);
-    return;
-  }
+__device__ __forceinline__ void prep_quant(const PrepArgs& a, int block, int blocks) {
+  const int KB = (a.q.cols + 127) / 128;
+  const int64_t groups = a.q.rows * KB;
+  constexpr int PER = kPrepThreads / 16;
+  for (int64_t g = (int64_t)block * PER; g < groups; g += (int64_t)blocks * PER) quant_group(a.q, g + (threadIdx.x >> 4), KB);
+}
+
+// Rows of each local expert among pairs p0 .. p1 - 1, into count (LDS, kPrepThreads words).
+__device__ __forceinline__ void prep_count(const PrepArgs& a, int p0, int p1, int* count) {
   static_assert(SMLP_MAX_EXPERTS <= kPrepThreads, "one thread per expert");
-  __shared__ int count[kPrepThreads], off[kPrepThreads], wsum[2][kPrepThreads / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  count[tid] = 0;
+  count[threadIdx.x] = 0;
   __syncthreads();
-  for (int p = tid; p < a.pairs; p += kPrepThreads) {
+  for (int p = p0 + (int)threadIdx.x; p < p1; p += kPrepThreads) {
     const int e = local_expert(a.ids[p], a.first, a.E);
     if (e >= 0) atomicAdd(&count[e], 1);
   }
   __syncthreads();
-  // Thread e: first sorted position and first tile of expert e, by a scan over the threads.
-  const int c = count[tid], nt = (c + a.bm - 1) / a.bm;
+}
+
+// Thread e holds expert e's rows c: its first sorted position, and (write) its tiles.
+__device__ __forceinline__ int prep_scan(const PrepArgs& a, int c, bool write, int (*wsum)[kPrepThreads / 64]) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int nt = (c + a.bm - 1) / a.bm;
   int o = c, t = nt;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -1552,19 +1557,24 @@ __global__ __launch_bounds__(kPrepThreads) void experts_prep_kernel(PrepArgs a) 
     o += wsum[0][v];
     t += wsum[1][v];
   }
-  if (tid == kPrepThreads - 1) a.hdr[0] = t;
-  off[tid] = o - c;
-  for (int i = 0, q = t - nt; i < c; i += a.bm, ++q) {
-    a.hdr[4 + 4 * q] = tid;
-    a.hdr[5 + 4 * q] = o - c + i;
-    a.hdr[6 + 4 * q] = min(a.bm, c - i);
+  if (write) {
+    if (tid == kPrepThreads - 1) a.hdr[0] = t;
+    for (int i = 0, q = t - nt; i < c; i += a.bm, ++q) {
+      a.hdr[4 + 4 * q] = tid;
+      a.hdr[5 + 4 * q] = o - c + i;
+      a.hdr[6 + 4 * q] = min(a.bm, c - i);
+    }
   }
-  __syncthreads();
-  // The order within an expert does not change any result (a row's sums do not depend on
-  // its place in a tile); rounds of the workgroup keep it near token order.
-  for (int p0 = 0; p0 < a.pairs; p0 += kPrepThreads) {
-    const int p = p0 + tid;
-    if (p < a.pairs) {
+  return o - c;
+}
+
+// Place pairs p0 .. p1 - 1 from the next free positions in off (LDS).  The order within an
+// expert does not change any result (a row's sums do not depend on its place in a tile);
+// rounds of the workgroup keep it near token order.
+__device__ __forceinline__ void prep_place(const PrepArgs& a, int p0, int p1, int* off) {
+  for (int q = p0; q < p1; q += kPrepThreads) {
+    const int p = q + (int)threadIdx.x;
+    if (p < p1) {
       const int e = local_expert(a.ids[p], a.first, a.E);
       const int at = e >= 0 ? atomicAdd(&off[e], 1) : -1;
       a.place[p] = at;
@@ -1572,6 +1582,44 @@ __global__ __launch_bounds__(kPrepThreads) void experts_prep_kernel(PrepArgs a) 
     }
     __syncthreads();
   }
+}
+
+__global__ __launch_bounds__(kPrepThreads) void experts_prep_kernel(PrepArgs a) {
+  if (blockIdx.x > 0) {
+    prep_quant(a, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  __shared__ int count[kPrepThreads], off[kPrepThreads], wsum[2][kPrepThreads / 64];
+  prep_count(a, 0, a.pairs, count);
+  off[threadIdx.x] = prep_scan(a, count[threadIdx.x], true, wsum);
+  __syncthreads();
+  prep_place(a, 0, a.pairs, off);
+}
+
+__global__ __launch_bounds__(kPrepThreads) void experts_count_kernel(PrepArgs a) {
+  const int b = blockIdx.x;
+  if (b >= a.chunks) {
+    prep_quant(a, b - a.chunks, gridDim.x - a.chunks);
+    return;
+  }
+  __shared__ int count[kPrepThreads];
+  prep_count(a, b * a.chunk, min(a.pairs, (b + 1) * a.chunk), count);
+  if ((int)threadIdx.x < a.E) a.counts[b * a.E + threadIdx.x] = count[threadIdx.x];
+}
+
+__global__ __launch_bounds__(kPrepThreads) void experts_place_kernel(PrepArgs a) {
+  __shared__ int off[kPrepThreads], wsum[2][kPrepThreads / 64];
+  const int b = blockIdx.x, e = threadIdx.x;
+  int all = 0, before = 0;
+  if (e < a.E)
+    for (int v = 0; v < a.chunks; ++v) {
+      const int c = a.counts[v * a.E + e];
+      all += c;
+      if (v < b) before += c;
+    }
+  off[e] = before + prep_scan(a, all, b == 0, wsum);
+  __syncthreads();
+  prep_place(a, b * a.chunk, min(a.pairs, (b + 1) * a.chunk), off);
 }
 
 // out[t] = sum_j weights[t, j] y[place of (t, j)] over the local experts, in fp32.
@@ -1589,28 +1637,62 @@ struct CombineArgs {
 __global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
   const int per = a.H / 8;
   const int64_t total = (int64_t)a.T * per;
+  constexpr int B = 8;  // pairs whose loads are in flight together
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int t = (int)(i / per), c = (int)(i - (int64_t)t * per) * 8;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < a.topk; ++j) {
-      const int at = a.place[(size_t)t * a.topk + j];
-      if (at < 0) continue;
-      float w = a.weights[(size_t)t * a.topk + j];
-      float v[8];
-      if (a.y_f32) {
-        load8(a.y, (size_t)at * a.H + c, 0, v);
-      } else {
-        const u32x4 u = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.y) + (size_t)at * a.H + c));
-        const float down = __uint_as_float((uint32_t)(a.yexp[(size_t)(c / 64) * a.P + at] - 14) << 23);
+    for (int j0 = 0; j0 < a.topk; j0 += B) {
+      int at[B];
+      float w[B];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          v[2 * q] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[q] & 0xffffu)) * down;
-          v[2 * q + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[q] >> 16)) * down;
+      for (int j = 0; j < B; ++j) {
+        const bool in = j0 + j < a.topk;
+        at[j] = in ? a.place[(size_t)t * a.topk + j0 + j] : -1;
+        w[j] = in ? a.weights[(size_t)t * a.topk + j0 + j] : 0.f;
+      }
+      if (a.y_f32) {
+        f32x4 y[B][2];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+          if (at[j] >= 0) {
+            const float* p = reinterpret_cast<const float*>(a.y) + (size_t)at[j] * a.H + c;
+            y[j][0] = *reinterpret_cast<const f32x4*>(p);
+            y[j][1] = *reinterpret_cast<const f32x4*>(p + 4);
+          }
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+          if (at[j] >= 0) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) acc[q] = fmaf(w[j], y[j][q >> 2][q & 3], acc[q]);
+          }
+      } else {
+        // Fewer at a time: the rows come from HBM, and more of them in flight were slower
+        // (65536 pairs of 7168: 8 at a time 240 us, 2 213 us).
+#pragma unroll
+        for (int j2 = 0; j2 < B; j2 += 2) {
+          u32x4 y[2];
+          uint32_t ex[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (at[j2 + j] >= 0) {
+              y[j] = __builtin_nontemporal_load(
+                  reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.y) + (size_t)at[j2 + j] * a.H + c));
+              ex[j] = a.yexp[(size_t)(c / 64) * a.P + at[j2 + j]];
+            }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (at[j2 + j] >= 0) {
+              const float down = __uint_as_float((ex[j] - 14u) << 23);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                acc[2 * q] = fmaf(w[j2 + j], (float)__builtin_bit_cast(_Float16, (uint16_t)(y[j][q] & 0xffffu)) * down, acc[2 * q]);
+                acc[2 * q + 1] = fmaf(w[j2 + j], (float)__builtin_bit_cast(_Float16, (uint16_t)(y[j][q] >> 16)) * down,
+                                      acc[2 * q + 1]);
+              }
+            }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
     }
     const size_t at = (size_t)t * a.H + c;
     if (a.out_f32) {
@@ -1844,8 +1926,17 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
   pa.q.s = xs;
   pa.q.s_row = 1;
   pa.q.s_kb = p.T;
-  hipLaunchKernelGGL(experts_prep_kernel, dim3(1 + quant_grid(p.T * HB, kPrepThreads / 16)), dim3(kPrepThreads), 0,
-                     s, pa);
+  pa.counts = reinterpret_cast<int*>(base + p.counts_off);
+  pa.chunk = p.chunk;
+  pa.chunks = p.chunk ? (pa.pairs + p.chunk - 1) / p.chunk : 1;
+  const unsigned qgrid = quant_grid(p.T * HB, kPrepThreads / 16);
+  if (!p.chunk) {
+    hipLaunchKernelGGL(experts_prep_kernel, dim3(1 + qgrid), dim3(kPrepThreads), 0, s, pa);
+  } else {
+    hipLaunchKernelGGL(experts_count_kernel, dim3((unsigned)pa.chunks + qgrid), dim3(kPrepThreads), 0, s, pa);
+    if (int e = (int)hipGetLastError()) return e;
+    hipLaunchKernelGGL(experts_place_kernel, dim3((unsigned)pa.chunks), dim3(kPrepThreads), 0, s, pa);
+  }
   int rc = (int)hipGetLastError();
   if (rc) return rc;
 

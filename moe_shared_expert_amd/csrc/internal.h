@@ -144,6 +144,8 @@ constexpr int kCUs = 256;  // compute units the grids are sized for
 // Limits of the short-K down kernel (16-row weight tiles per workgroup) and of the kernels
 // for one token (blocks of 128 in H; blocks of 128 in I over all pairs).
 constexpr int kDownRun = 496, kTokenBlocks = 64, kTokenPairBlocks = 64;
+// Most pairs that one workgroup sorts, and most chunks otherwise.
+constexpr int kOneSort = 4096, kSortChunks = 64;
 // Most K slices of the projection of up to 16 rows, and its columns of workgroups then.
 constexpr int kNarrowSlices = 8, kNarrowColumns = 256;
 
@@ -181,9 +183,10 @@ struct ExpertsPlan {
   int64_t P;            // pairs = T * topk
   int64_t max_tiles;    // row tiles that any routing can need
   F8Plan gu, dn;
+  int chunk;            // pairs per workgroup of the sort in two launches (0: one workgroup)
   int token;            // one token: two launches without a sort
   int y_f32;            // rows of y held in fp32 (1) or fp16 with exponents (0)
-  size_t hdr_off, perm_off, place_off, yexp_off, x8_off, xs_off, h8_off, hs_off, h32_off, y_off, workspace_bytes;
+  size_t hdr_off, perm_off, place_off, counts_off, yexp_off, x8_off, xs_off, h8_off, hs_off, h32_off, y_off, workspace_bytes;
 };
 struct ExpertsCall {
   const void* x;

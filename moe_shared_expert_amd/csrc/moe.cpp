@@ -150,7 +150,7 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
   const int64_t HB = blocks128(H), IB = blocks128(I);
   const int64_t active = p.P < E ? p.P : E;
   const int64_t rows = active ? p.P / active : 0;
-  if (rows <= 24) {
+  if (rows <= 12) {
     p.gu = stream_plan(rows * 2, HB);
     p.dn = stream_plan(rows * 2, IB);
     if (IB * p.dn.bm <= 256) {
@@ -179,6 +179,11 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
   };
   p.hdr_off = take((size_t)(4 + 4 * p.max_tiles) * 4);
   p.perm_off = take((size_t)p.P * 4);
+  if (p.P > smlp::kOneSort) {
+    const int64_t least = (p.P + smlp::kSortChunks - 1) / smlp::kSortChunks;
+    p.chunk = (int)(least < 2048 ? 2048 : (least + 1023) / 1024 * 1024);
+  }
+  p.counts_off = take(p.chunk ? (size_t)smlp::kSortChunks * (size_t)E * 4 : 0);
   p.place_off = take((size_t)p.P * 4);
   p.yexp_off = take(p.y_f32 ? 0 : (size_t)p.P * (size_t)((H + 63) / 64));
   p.x8_off = take((size_t)(T * H));

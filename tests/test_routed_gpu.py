@@ -251,6 +251,7 @@ EXPERTS = [  # T, H, I, E, k, experts the ids range over
     (1, 16, 16, 1, 1, 1), (1, 256, 128, 8, 4, 8), (2, 272, 144, 5, 2, 5), (7, 512, 336, 3, 3, 9),
     (40, 400, 256, 16, 4, 16), (33, 128, 400, 2, 1, 2), (70, 256, 128, 4, 2, 4), (130, 384, 272, 3, 2, 6),
     (300, 144, 128, 2, 2, 2), (520, 256, 160, 2, 1, 2), (64, 128, 128, 64, 8, 64), (24, 640, 128, 300, 6, 300),
+    (1700, 64, 48, 5, 3, 7),
 ]
 
 
