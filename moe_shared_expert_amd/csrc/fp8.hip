@@ -55,7 +55,8 @@ struct F8Args {
   int hs_ld;
   uint8_t* yexp;       // down with fp16 y: exponent of position p and columns 64 c .. + 63 at
                        // yexp[c * hs_ld + p]
-  float* part;         // projection with a K split: fp32 partials [slices][M][N]
+  float* part;         // projection with a K split: fp32 partials, and one arrival counter per
+  uint32_t* arrived;   // tile, 16 words apart, zero between launches
   int kslice;          // K blocks per slice
 };
 
@@ -585,14 +586,14 @@ __global__ __launch_bounds__(512, 2) void f8_narrow_kernel(NarrowArgs a) {
     __syncthreads();
     if (!last || wave >= NT) return;
     const __amdgpu_buffer_rsrc_t pr = make_rsrc(g.part, (uint32_t)(slices * step * 4));
-    f32x4 v[kNarrowSlices];
+    f32x4 v[kSlices];
 #pragma unroll
-    for (int q = 0; q < kNarrowSlices; ++q)
+    for (int q = 0; q < kSlices; ++q)
       v[q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
                  pr, (int)(q < slices ? (uint32_t)((q * step + col) * 4) : kNoRow), 0, 16));
     sum = v[0];
 #pragma unroll
-    for (int q = 1; q < kNarrowSlices; ++q) sum += v[q];  // slices past the last are zeros
+    for (int q = 1; q < kSlices; ++q) sum += v[q];  // slices past the last are zeros
   }
   if (wave >= NT) return;
   const int n = n0 + 16 * wave + 4 * lg;
@@ -1245,6 +1246,45 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
     }
     int stores = 0;  // known when inlined; -1: not fixed
     const int lane = fresh(), ln = lane & 15, lg = lane >> 4;
+    if constexpr (MODE == F8_LINEAR) {
+      if (gridDim.y > 1) {
+        // K split over workgroups (one tile each, at most kReduceTiles): this slice's sums go
+        // out agent-coherent as [slice][tile][row tile, column tile][lane][4]; the last slice
+        // of a tile to arrive adds all of them in slice order and goes on with the sum.
+        const uint32_t tile = blockIdx.x, per = BM * BN * 4, step = gridDim.x * per;
+        const __amdgpu_buffer_rsrc_t pr = make_rsrc(g.part, gridDim.y * step);
+        const uint32_t base = tile * per + (uint32_t)(wave * TM * TN * 64 + lane) * 16u;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), pr,
+                                                   (int)(blockIdx.y * step + base + (i * TN + j) * 1024), 0, 16);
+        wait_vmcnt<0>();
+        f8_barrier();
+        int* last = reinterpret_cast<int*>(lds + NS * STAGE);
+        if (threadIdx.x == 0) {
+          uint32_t* c = g.arrived + 16 * tile;
+          const bool l = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.y - 1;
+          if (l) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          *reinterpret_cast<volatile int*>(last) = l;
+        }
+        __syncthreads();
+        if (!*reinterpret_cast<volatile int*>(last)) return;
+        __syncthreads();  // the flag is read before the staging area is used
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (uint32_t q = 0; q < gridDim.y; ++q)
+#pragma unroll
+          for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+              acc[i][j] += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                               pr, (int)(q * step + base + (i * TN + j) * 1024), 0, 16));
+      }
+    }
     char* const stg = lds + NS * STAGE + wave * (16 * PITCH);
     if constexpr (GU) {
       // h = SiLU(gate) * up, then e4m3 with one scale per row and 128 features: the rows'
@@ -1313,10 +1353,9 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
       stores = TM / 4 + TM / 2;
     } else {
       constexpr int CPR = 2 * TN, RPI = 64 / CPR;  // 16-byte chunks per staged row, rows per store
-      const bool split = MODE == F8_LINEAR && gridDim.y > 1;
       const bool whole = MODE == F8_DOWN
                              ? !g.out_f32
-                             : !g.out_f32 && !split && cur.f0 + FN <= g.N && g.ldo % 8 == 0 && ((uintptr_t)g.out & 15) == 0;
+                             : !g.out_f32 && cur.f0 + FN <= g.N && g.ldo % 8 == 0 && ((uintptr_t)g.out & 15) == 0;
       if (whole) {
         // Rows through LDS: a lane's four features are 8 bytes of 16 different rows, the
         // stores below whole runs of 32 TN bytes per row.  Projection: bf16.  Experts: fp16
@@ -1382,14 +1421,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
           for (int j = 0; j < TN; ++j) {
             const int n = cur.f0 + (wn * TN + j) * 16 + 4 * lg;
             if (n >= g.N) continue;
-            if (split) {
-              float* p = g.part + ((size_t)blockIdx.y * g.M + row) * (size_t)g.N + n;
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (n + e < g.N) p[e] = acc[i][j][e];
-            } else {
-              f8_store4(g, row, n, acc[i][j]);
-            }
+            f8_store4(g, row, n, acc[i][j]);
           }
         }
       }
@@ -1402,19 +1434,6 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
     else wait_vmcnt<0>();
     lin += (int)gridDim.x;
     cur = nxt_place;
-  }
-}
-
-// Sum of the K slices' partials in slice order.
-__global__ __launch_bounds__(256) void f8_join_kernel(const float* part, int slices, int M, int N, void* out,
-                                                      int ldo, int out_f32) {
-  const size_t total = (size_t)M * N;
-  for (size_t e = blockIdx.x * (size_t)256 + threadIdx.x; e < total; e += (size_t)gridDim.x * 256) {
-    float v = part[e];
-    for (int q = 1; q < slices; ++q) v += part[q * total + e];
-    const size_t at = e / N * ldo + e % N;
-    if (out_f32) reinterpret_cast<float*>(out)[at] = v;
-    else reinterpret_cast<uint16_t*>(out)[at] = (uint16_t)f2bf(v);
   }
 }
 
@@ -1812,8 +1831,7 @@ int launch_narrow_fp8(const F8Plan& p, const void* x, const void* w, const float
   a.g.kslice = slices > 1 ? p.kslice : a.g.KB;
   a.g.part = part;
   const dim3 grid((unsigned)cols, (unsigned)slices);
-  if (p.nt == 1) hipLaunchKernelGGL((f8_narrow_kernel<1, 4>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((f8_narrow_kernel<2, 3>), grid, dim3(512), 0, s, a);
+  hipLaunchKernelGGL((f8_narrow_kernel<1, 4>), grid, dim3(512), 0, s, a);
   return (int)hipGetLastError();
 }
 
@@ -1838,15 +1856,17 @@ int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t 
   g.ldo = (int)ldy;
   g.out_f32 = out_f32;
   g.part = part;
-  g.kslice = p.kslice;
   const int tiles = (int)((M + p.bm - 1) / p.bm);
-  int rc = launch_f8<F8_LINEAR>(p, g, tiles, s);
-  if (rc || p.ksplit == 1) return rc;
-  const int64_t total = M * N;
-  const int64_t blocks = (total + 255) / 256;
-  hipLaunchKernelGGL(f8_join_kernel, dim3((unsigned)(blocks > 4096 ? 4096 : blocks)), dim3(256), 0, s, part,
-                     p.ksplit, (int)M, (int)N, y, (int)ldy, out_f32);
-  return (int)hipGetLastError();
+  F8Plan q = p;
+  if (p.ksplit > 1) {
+    g.arrived = reduce_counters(s, (int)(tiles * ((N + p.bn - 1) / p.bn)));
+    if (!g.arrived) {  // no counters left for this stream: no split
+      q.ksplit = 1;
+      q.kslice = g.KB;
+    }
+  }
+  g.kslice = q.kslice;
+  return launch_f8<F8_LINEAR>(q, g, tiles, s);
 }
 
 namespace {

@@ -146,8 +146,8 @@ constexpr int kCUs = 256;  // compute units the grids are sized for
 constexpr int kDownRun = 496, kTokenBlocks = 64, kTokenPairBlocks = 64;
 // Most pairs that one workgroup sorts, and most chunks otherwise.
 constexpr int kOneSort = 4096, kSortChunks = 64;
-// Most K slices of the projection of up to 16 rows, and its columns of workgroups then.
-constexpr int kNarrowSlices = 8, kNarrowColumns = 256;
+// Most K slices of a projection, and most tiles (columns of workgroups) with a K split.
+constexpr int kSlices = 8, kReduceTiles = 256;
 
 // One 8-bit block-scaled product (fp8.hip).
 enum { F8_KIND_STREAM = 0, F8_KIND_TILE = 1, F8_KIND_DOWN = 2, F8_KIND_ROW = 3, F8_KIND_NARROW = 4 };

@@ -90,20 +90,22 @@ int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, L
     p.f = stream_plan(M, KB);
     p.f.kind = smlp::F8_KIND_ROW;  // x is brought to its 8-bit form in each workgroup
     x_fp8 = 1;
-  } else if (M <= 16 && !x_fp8 && M * K < kLimit / 2) {
+  } else if (M <= 16 && N <= 1536 && !x_fp8 && M * K < kLimit / 2) {
+    // Few rows of w: x is brought to its 8-bit form by the workgroups that use it (16 x 512 x
+    // 7168: 6.8 us against 14 us with a launch of its own; at N = 2112 both take 14 us).
     p.f = stream_plan(M, KB);
     p.f.kind = smlp::F8_KIND_NARROW;
-    p.f.nt = N > 16 * 2 * smlp::kCUs ? 2 : 1;
-    x_fp8 = 1;  // likewise
+    p.f.nt = 1;
+    x_fp8 = 1;
     // Up to two workgroups per compute unit, at least one block per wave.
-    const int64_t cols = (N + 16 * p.f.nt - 1) / (16 * p.f.nt);
+    const int64_t cols = (N + 15) / 16;
     int64_t slices = 2 * smlp::kCUs / cols;
     if (slices > (KB + 7) / 8) slices = (KB + 7) / 8;
-    if (slices > smlp::kNarrowSlices) slices = smlp::kNarrowSlices;
-    if (slices > 1 && cols <= smlp::kNarrowColumns) {
+    if (slices > smlp::kSlices) slices = smlp::kSlices;
+    if (slices > 1) {
       p.f.kslice = (int)((KB + slices - 1) / slices);
       p.f.ksplit = (int)((KB + p.f.kslice - 1) / p.f.kslice);
-      part = (size_t)p.f.ksplit * (size_t)(cols * p.f.nt) * 256 * 4;
+      part = (size_t)p.f.ksplit * (size_t)cols * 256 * 4;
     }
   } else if (M <= 32) {
     p.f = stream_plan(M, KB);
@@ -115,6 +117,20 @@ int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, L
     const int exact = out_fp32 || KB <= 4;
     const int b = t256 >= 256 ? 256 : t128 >= 256 ? 128 : 64;
     p.f = tile_plan(b, b, KB, exact);
+    const int64_t tiles = ((M + b - 1) / b) * ((N + b - 1) / b);
+    if (b == 64 && 2 * tiles <= smlp::kCUs) {
+      // Not even one tile for every second compute unit: K over workgroups too, at least
+      // eight blocks each (64 x 7168 x 7168: 20.6 -> 16.9 us; with more tiles or shorter
+      // slices the second pass over the sums costs what the split saves).
+      int64_t slices = 2 * smlp::kCUs / tiles;
+      if (slices > KB / 8) slices = KB / 8;
+      if (slices > smlp::kSlices) slices = smlp::kSlices;
+      if (slices > 1) {
+        p.f.kslice = (int)((KB + slices - 1) / slices);
+        p.f.ksplit = (int)((KB + p.f.kslice - 1) / p.f.kslice);
+        part = (size_t)p.f.ksplit * (size_t)tiles * 64 * 64 * 4;
+      }
+    }
   }
   size_t off = 0;
   p.x8_off = off;
@@ -122,7 +138,6 @@ int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, L
   p.xs_off = off;
   if (!x_fp8) off += round_up((size_t)(M * KB) * 4);
   p.part_off = off;
-  if (p.f.kind == smlp::F8_KIND_TILE && p.f.ksplit > 1) part = (size_t)p.f.ksplit * (size_t)(M * N) * 4;
   off += round_up(part);
   p.workspace_bytes = off;
   *out = p;
