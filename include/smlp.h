@@ -290,6 +290,11 @@ int shared_mlp_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t N, int x
  * K a positive multiple of 16; N >= 1; ldy >= N; M * K, N * K and M * ldy < 2^31; x and w
  * 16-byte aligned, y aligned to its element; workspace 256-byte aligned (may be NULL when
  * 0 bytes are needed).  y must not overlap an input or the workspace.  M == 0 is a no-op.
+ * Products are exact and summed in fp32, except where M > 32, K > 512 and y is bf16: there
+ * the 8-bit matrix instructions are used, whose sum over a block of 128 is about 1.4e-5 off.
+ * Like shared_mlp_linear, a product whose K is split over workgroups (few outputs) counts
+ * arrivals per stream (16 streams per GPU; further ones run without the split), so two
+ * replays of one captured graph must not run at the same time.
  */
 int shared_mlp_linear_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* y,
                           int64_t M, int64_t K, int64_t N, int64_t ldy, int out_fp32, void* workspace,

@@ -514,6 +514,21 @@ def _queue(stream, index):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on(stream):
+    """Context in which torch allocates for `stream`, so that scratch memory freed when a call
+    returns is reused only behind the work that uses it."""
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+def _scratch(need, device, stream):
+    if not need:
+        return None
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    with _on(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
 def _blocks128(n: int) -> int:
     return (n + 127) // 128
 
@@ -546,12 +561,14 @@ def shared_mlp_route(logits, ids, weights, score="sigmoid", bias=None, groups=1,
 
 def route(logits, topk: int, score="sigmoid", bias=None, groups=1, top_groups=None, group_top=1, renormalize=True,
           scale=1.0, stream=None):
-    """Allocating form of shared_mlp_route; returns ids, weights."""
+    """Allocating form of shared_mlp_route; returns ids, weights (allocated for `stream`)."""
+    if stream is not None:
+        with _on(stream):
+            return route(logits, topk, score, bias, groups, top_groups, group_top, renormalize, scale)
     if score not in ROUTE_SCORES:
         raise ValueError(f"score {score!r} is not one of {sorted(ROUTE_SCORES)}")
     return (_calls or _load_calls()).route(logits, topk, ROUTE_SCORES[score], bias, groups,
-                                           groups if top_groups is None else top_groups, group_top, renormalize, scale,
-                                           None if stream is None else _queue(stream, 0))
+                                           groups if top_groups is None else top_groups, group_top, renormalize, scale)
 
 
 def shared_mlp_quant_fp8(x, q, scales, block_rows=1, stream=None):
@@ -606,7 +623,7 @@ def shared_mlp_linear_fp8(x, w, w_scales, y, x_scales=None, workspace=None, stre
     dev = x.get_device()
     if workspace is None:
         need = shared_mlp_linear_fp8_workspace_bytes(M, K, N, quantized)
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        workspace = _scratch(need, x.device, stream)
     _same_device(dev, x_scales, w, w_scales, y, workspace)
     rc = lib().shared_mlp_linear_fp8(xp, xsp, wp, wsp, yp, M, K, N, ldy, out_fp32, _ptr(workspace),
                                      _ws_bytes(workspace), _queue(stream, dev))
@@ -616,9 +633,11 @@ def shared_mlp_linear_fp8(x, w, w_scales, y, x_scales=None, workspace=None, stre
 
 
 def linear_fp8(x, w, w_scales, x_scales=None, out_fp32=False, workspace=None, stream=None):
-    """Allocating form of shared_mlp_linear_fp8."""
-    return (_calls or _load_calls()).linear_fp8(x, w, w_scales, x_scales, out_fp32, workspace,
-                                                None if stream is None else _queue(stream, 0))
+    """Allocating form of shared_mlp_linear_fp8 (y and any workspace allocated for `stream`)."""
+    if stream is not None:
+        with _on(stream):
+            return linear_fp8(x, w, w_scales, x_scales, out_fp32, workspace)
+    return (_calls or _load_calls()).linear_fp8(x, w, w_scales, x_scales, out_fp32, workspace)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -646,7 +665,7 @@ def shared_mlp_experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down
             _want("s_down", s_down, torch.float32, (E, HB, IB)), _want("out", out, out.dtype, (T, H)))
     if workspace is None:
         need = shared_mlp_experts_fp8_workspace_bytes(T, H, I, E, topk, partial)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+        workspace = _scratch(max(need, 256), x.device, stream)
     _same_device(dev, ids, weights, w_gate_up, s_gate_up, w_down, s_down, out, workspace)
     rc = lib().shared_mlp_experts_fp8(*args, T, H, I, E, topk, first_expert, partial, _ptr(workspace),
                                       _ws_bytes(workspace), _queue(stream, dev))
@@ -657,10 +676,13 @@ def shared_mlp_experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down
 
 def experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert=0, partial_fp32=False,
                 workspace=None, stream=None):
-    """Allocating form of shared_mlp_experts_fp8."""
+    """Allocating form of shared_mlp_experts_fp8 (out and any workspace allocated for `stream`)."""
+    if stream is not None:
+        with _on(stream):
+            return experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert, partial_fp32,
+                               workspace)
     return (_calls or _load_calls()).experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert,
-                                                 partial_fp32, workspace,
-                                                 None if stream is None else _queue(stream, 0))
+                                                 partial_fp32, workspace)
 
 
 # Measurement kernels (include/smlp_ceilings.h): launch them, time them on the caller's side.

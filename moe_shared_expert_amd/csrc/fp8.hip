@@ -1244,6 +1244,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
       aim(nxt_place);
       first_loads();
     }
+    __builtin_amdgcn_sched_barrier(0);  // the stores below stay behind these loads
     int stores = 0;  // known when inlined; -1: not fixed
     const int lane = fresh(), ln = lane & 15, lg = lane >> 4;
     if constexpr (MODE == F8_LINEAR) {

@@ -168,7 +168,7 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
   if (rows <= 12) {
     p.gu = stream_plan(rows * 2, HB);
     p.dn = stream_plan(rows * 2, IB);
-    if (IB * p.dn.bm <= 256) {
+    if (IB * p.dn.bm <= 256 && IB <= 16) {
       // The whole K of a tile's activations fits LDS: about four workgroups per compute unit
       // over the (tile, run of weight tiles) pairs, at least four weight tiles each.
       p.dn.kind = smlp::F8_KIND_DOWN;

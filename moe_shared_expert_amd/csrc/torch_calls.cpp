@@ -51,10 +51,8 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
-hipStream_t queue(PyObject* o, int dev) {
-  if (o == Py_None) return c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).stream();
-  return reinterpret_cast<hipStream_t>((uintptr_t)integer(o));
-}
+// Work and allocations go to the current stream (the binding makes a caller's stream current).
+hipStream_t queue(int dev) { return c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).stream(); }
 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
@@ -88,9 +86,9 @@ bool counted(Py_ssize_t n, Py_ssize_t want) {
   return false;
 }
 
-// route(logits, topk, score, bias, groups, top_groups, group_top, renormalize, scale, stream)
+// route(logits, topk, score, bias, groups, top_groups, group_top, renormalize, scale)
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!counted(n, 10)) return nullptr;
+  if (!counted(n, 9)) return nullptr;
   return guarded([&]() -> PyObject* {
     const at::Tensor& logits = tensor(a[0], "logits");
     if (logits.dim() != 2 || !logits.is_cuda() || (logits.size(1) > 1 && logits.stride(1) != 1))
@@ -109,7 +107,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor ids = fresh({T, topk}, at::kInt, logits), weights = fresh({T, topk}, at::kFloat, logits);
     checked(shared_mlp_route(logits.data_ptr(), type == at::kFloat ? SMLP_FP32 : SMLP_BF16, T, E,
                              T > 1 ? logits.stride(0) : E, bias, &r, static_cast<int32_t*>(ids.data_ptr()),
-                             static_cast<float*>(weights.data_ptr()), queue(a[9], dev)));
+                             static_cast<float*>(weights.data_ptr()), queue(dev)));
     PyObject* i = THPVariable_Wrap(std::move(ids));
     PyObject* w = THPVariable_Wrap(std::move(weights));
     PyObject* both = PyTuple_Pack(2, i, w);
@@ -134,9 +132,9 @@ void* scratch(PyObject* given, size_t need, const at::Tensor& like, at::Tensor& 
   return own.data_ptr();
 }
 
-// linear_fp8(x, w, w_scales, x_scales, out_fp32, workspace, stream)
+// linear_fp8(x, w, w_scales, x_scales, out_fp32, workspace)
 PyObject* linear_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!counted(n, 7)) return nullptr;
+  if (!counted(n, 6)) return nullptr;
   return guarded([&]() -> PyObject* {
     const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w");
     if (x.dim() != 2 || w.dim() != 2) throw Refused{"x and w must be matrices"};
@@ -153,14 +151,14 @@ PyObject* linear_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor own;
     void* ws = scratch(a[5], need, x, own, bytes);
     at::Tensor y = fresh({M, N}, f32 ? at::kFloat : at::kBFloat16, x);
-    checked(shared_mlp_linear_fp8(xp, xsp, wp, wsp, y.data_ptr(), M, K, N, N, f32, ws, bytes, queue(a[6], dev)));
+    checked(shared_mlp_linear_fp8(xp, xsp, wp, wsp, y.data_ptr(), M, K, N, N, f32, ws, bytes, queue(dev)));
     return THPVariable_Wrap(std::move(y));
   });
 }
 
-// experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert, partial_fp32, workspace, stream)
+// experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert, partial_fp32, workspace)
 PyObject* experts_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!counted(n, 11)) return nullptr;
+  if (!counted(n, 10)) return nullptr;
   return guarded([&]() -> PyObject* {
     const at::Tensor &x = tensor(a[0], "x"), &ids = tensor(a[1], "ids"), &wd = tensor(a[5], "w_down");
     if (x.dim() != 2 || ids.dim() != 2 || wd.dim() != 3) throw Refused{"x and ids must be matrices, w_down [E, H, I]"};
@@ -182,7 +180,7 @@ PyObject* experts_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor out = fresh({T, H}, f32 ? at::kFloat : at::kBFloat16, x);
     checked(shared_mlp_experts_fp8(xp, static_cast<const int32_t*>(ip), static_cast<const float*>(rp), gp,
                                    static_cast<const float*>(gs), dp, static_cast<const float*>(ds), out.data_ptr(), T,
-                                   H, I, E, topk, integer(a[7]), f32, ws, bytes, queue(a[10], dev)));
+                                   H, I, E, topk, integer(a[7]), f32, ws, bytes, queue(dev)));
     return THPVariable_Wrap(std::move(out));
   });
 }

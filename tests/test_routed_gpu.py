@@ -159,7 +159,7 @@ def test_quantize_parts_strides_and_special_values():
 # ------------------------------------------------------------------ the product
 
 LINEARS = [(1, 16, 1), (1, 128, 132), (3, 144, 17), (16, 7168, 132), (17, 1024, 130), (32, 400, 257), (33, 384, 96),
-           (64, 2000, 300), (129, 256, 127), (200, 768, 1031), (257, 1040, 512), (300, 128, 4096), (1100, 272, 260)]
+           (64, 2000, 300), (129, 256, 127), (1, 8208, 40), (200, 768, 1031), (257, 1040, 512), (300, 128, 4096), (1100, 272, 260)]
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8"])
@@ -184,6 +184,44 @@ def test_linear(size, out_fp32, fmt):
     tol = (128 + routed.blocks(K) + 4) * U * size_ + (0 if out_fp32 else 2.0 ** -8 * np.abs(ref))
     err = np.abs(f64(y[:, :N]) - ref)
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+def test_linear_on_many_streams():
+    """The K split keeps counters for a limited number of streams; further streams do without."""
+    g = gen(21)
+    x = randn(g, 16, 4096).bfloat16().to(DEV)
+    xl = randn(g, 64, 4096).bfloat16().to(DEV)
+    wq, ws = binding.quantize_fp8(randn(g, 132, 4096).to(DEV), 128)
+    one, many = binding.linear_fp8(x, wq, ws, out_fp32=True), binding.linear_fp8(xl, wq, ws, out_fp32=True)
+    torch.cuda.synchronize()
+    for s in [torch.cuda.Stream() for _ in range(24)]:
+        a, b = binding.linear_fp8(x, wq, ws, out_fp32=True, stream=s), binding.linear_fp8(xl, wq, ws, out_fp32=True, stream=s)
+        s.synchronize()
+        assert (a - one).abs().max() <= 1e-5 * one.abs().max() and (b - many).abs().max() <= 1e-5 * many.abs().max()
+
+
+def test_allocating_forms_equal_the_others_on_any_stream():
+    d = make_experts(14, 20, 256, 128, 8, 2)
+    logits = randn(gen(2), 20, 8).to(DEV)
+    want = run_experts(d)
+    ids, w = torch.empty_like(d["ids"]), torch.empty_like(d["weights"])
+    binding.shared_mlp_route(logits, ids, w, score="softmax")
+    args = (d["x"], d["ids"], d["weights"], d["qgu"], d["sgu"], d["qd"], d["sd"])
+    torch.cuda.synchronize()
+    for stream in (None, torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        got = [binding.route(logits, 2, score="softmax", stream=stream), binding.experts_fp8(*args, stream=stream)]
+        out = torch.empty_like(want)
+        binding.shared_mlp_experts_fp8(*args, out, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0][0], ids) and torch.equal(got[0][1], w)
+        assert torch.equal(got[1], want) and torch.equal(out, want)
+    with pytest.raises(ValueError):
+        binding.experts_fp8(*args[:1], args[1].long(), *args[2:])
+    with pytest.raises(binding.SmlpError):
+        binding.route(logits, 9)
+    with pytest.raises(binding.SmlpError):
+        binding.linear_fp8(d["x"][:, :24].contiguous(), torch.zeros(8, 24, device=DEV).to(binding.FP8),
+                           torch.ones(1, 1, device=DEV))
 
 
 def test_linear_nan_stays_in_its_row():
@@ -251,7 +289,8 @@ EXPERTS = [  # T, H, I, E, k, experts the ids range over
     (1, 16, 16, 1, 1, 1), (1, 256, 128, 8, 4, 8), (2, 272, 144, 5, 2, 5), (7, 512, 336, 3, 3, 9),
     (40, 400, 256, 16, 4, 16), (33, 128, 400, 2, 1, 2), (70, 256, 128, 4, 2, 4), (130, 384, 272, 3, 2, 6),
     (300, 144, 128, 2, 2, 2), (520, 256, 160, 2, 1, 2), (64, 128, 128, 64, 8, 64), (24, 640, 128, 300, 6, 300),
-    (1700, 64, 48, 5, 3, 7),
+    (1700, 64, 48, 5, 3, 7), (6, 144, 2320, 3, 2, 3), (5, 128, 1296, 4, 1, 4), (1, 8208, 128, 2, 2, 2),
+    (1, 144, 2320, 9, 8, 12),
 ]
 
 
