@@ -45,6 +45,11 @@ ROUTES = [
     (9, 512, 16, dict(score="sigmoid", groups=64, top_groups=9, group_top=2)),
     (3, 1024, 2, dict(score="sigmoid", bias=True, groups=2, top_groups=1)),
     (1027, 160, 6, dict(score="sigmoid", bias=True, groups=8, top_groups=3, group_top=2)),
+    # many tokens
+    (2049, 256, 8, dict(score="sigmoid", bias=True, groups=8, top_groups=4, group_top=2, scale=2.5)),
+    (2051, 96, 5, dict(score="softmax", groups=32, top_groups=7)),
+    (2100, 33, 32, dict(score="softmax")),
+    (2048, 20, 3, dict(score="sigmoid", groups=2, top_groups=1, group_top=2)),
 ]
 
 
