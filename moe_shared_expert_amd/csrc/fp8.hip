@@ -958,7 +958,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave % WM, wn = wave / WM;
+  const int wm = wave / WN, wn = wave % WN;  // the waves that share a SIMD have different rows
   const int ln = lane & 15, lg = lane >> 4, lr = lane >> 3;
   const int tiles_m = MODE == F8_LINEAR ? g.tiles_m : g.hdr[0];
   const int K = g.K;
@@ -1147,7 +1147,10 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
           const int m = i * TN + j;
+          // The matrix instruction goes first whenever both waves of a SIMD have something to issue.
+          __builtin_amdgcn_s_setprio(1);
           p[m & 3] = mfma_fp8(wf[j], af[i & 1]);
+          __builtin_amdgcn_s_setprio(0);
           madd((m + SLOTS - 2) % SLOTS);
           if (last) read_wf(nst, j);
           if (j == 0) {
@@ -1171,7 +1174,19 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
         }
         scales_of(s_next, ri & 1);
       };
-      {
+      // A wave none of whose rows exist only moves data (an expert's last tile): the other wave
+      // of its SIMD has the matrix core to itself.
+      const bool idle = WM > 1 && wm * TM * 16 >= cur.count;
+      if (idle) {
+        for (int kt = 0; kt < nk; ++kt) {
+#pragma unroll
+          for (int l = HALF; l < LPS; ++l) issue_one((kt + NS - 1) % NS, kb0 + kt + NS - 1, l);
+          wait_vmcnt<(NS - 2) * LPS>();
+          f8_barrier();
+#pragma unroll
+          for (int l = 0; l < HALF; ++l) issue_one(kt % NS, kb0 + kt + NS, l);
+        }
+      } else {
         const char* st = lds;
         const float* w2 = reinterpret_cast<const float*>(st + A_BYTES + B_BYTES + wave * 256 + 128);
         swg = w2[0];
@@ -1183,7 +1198,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
         scales_of(row_scale(st + A_BYTES + B_BYTES, 0), 0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      for (int kt = 0; kt < nk; ++kt) {
+      for (int kt = 0; kt < (idle ? 0 : nk); ++kt) {
         const int now = kt % NS, nxt = (kt + 1) % NS;
         const char* st = lds + now * STAGE;
         const char* nst = lds + nxt * STAGE;
@@ -1201,8 +1216,10 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
         row_tile(TM - 1, st, nst, now, kb0 + kt + NS, 0, HALF);
       }
       // The last two slots' multiply-adds; sg / su of the last row tile are still in place.
-      madd(SLOTS - 2);
-      madd(SLOTS - 1);
+      if (!idle) {
+        madd(SLOTS - 2);
+        madd(SLOTS - 1);
+      }
       __builtin_amdgcn_s_waitcnt(0xc07f);
     } else {
       for (int kt = 0; kt < nk; ++kt) {
