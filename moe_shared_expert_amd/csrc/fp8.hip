@@ -1662,7 +1662,6 @@ __global__ __launch_bounds__(kPrepThreads) void experts_place_kernel(PrepArgs a)
 // out[t] = sum_j weights[t, j] y[place of (t, j)] over the local experts, in fp32.
 struct CombineArgs {
   const void* y;         // fp32, or fp16 with exponents
-  int y_f32;
   const uint8_t* yexp;
   int P;
   const int* place;
@@ -1671,10 +1670,14 @@ struct CombineArgs {
   int T, H, topk, out_f32;
 };
 
+// F32: few pairs, whose latency counts: a token's places and rows are loaded together (32
+// tokens of 8 pairs: 6.5 -> 4.5 us).  Otherwise the rows come from HBM, one after the other
+// (8192 tokens of 8 pairs of 7168: 215 us for 1.06 GB; two at a time behind branches 370 us).
+template <bool F32>
 __global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
   const int per = a.H / 8;
   const int64_t total = (int64_t)a.T * per;
-  constexpr int B = 8;  // pairs whose loads are in flight together
+  constexpr int B = F32 ? 8 : 1;  // pairs whose loads are in flight together
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int t = (int)(i / per), c = (int)(i - (int64_t)t * per) * 8;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -1687,7 +1690,7 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
         at[j] = in ? a.place[(size_t)t * a.topk + j0 + j] : -1;
         w[j] = in ? a.weights[(size_t)t * a.topk + j0 + j] : 0.f;
       }
-      if (a.y_f32) {
+      if constexpr (F32) {
         f32x4 y[B][2];
 #pragma unroll
         for (int j = 0; j < B; ++j)
@@ -1703,31 +1706,16 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
             for (int q = 0; q < 8; ++q) acc[q] = fmaf(w[j], y[j][q >> 2][q & 3], acc[q]);
           }
       } else {
-        // Fewer at a time: the rows come from HBM, and more of them in flight were slower
-        // (65536 pairs of 7168: 8 at a time 240 us, 2 213 us).
+        if (at[0] < 0) continue;
+        const u32x4 u = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.y) + (size_t)at[0] * a.H + c));
+        const float down = __uint_as_float((uint32_t)(a.yexp[(size_t)(c / 64) * a.P + at[0]] - 14) << 23);
 #pragma unroll
-        for (int j2 = 0; j2 < B; j2 += 2) {
-          u32x4 y[2];
-          uint32_t ex[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (at[j2 + j] >= 0) {
-              y[j] = __builtin_nontemporal_load(
-                  reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.y) + (size_t)at[j2 + j] * a.H + c));
-              ex[j] = a.yexp[(size_t)(c / 64) * a.P + at[j2 + j]];
-            }
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (at[j2 + j] >= 0) {
-              const float down = __uint_as_float((ex[j] - 14u) << 23);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                acc[2 * q] = fmaf(w[j2 + j], (float)__builtin_bit_cast(_Float16, (uint16_t)(y[j][q] & 0xffffu)) * down, acc[2 * q]);
-                acc[2 * q + 1] = fmaf(w[j2 + j], (float)__builtin_bit_cast(_Float16, (uint16_t)(y[j][q] >> 16)) * down,
-                                      acc[2 * q + 1]);
-              }
-            }
-          __builtin_amdgcn_sched_barrier(0);
+        for (int q = 0; q < 4; ++q) {
+          const float lo = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[q] & 0xffffu));
+          const float hi = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[q] >> 16));
+          acc[2 * q] = fmaf(w[0], lo * down, acc[2 * q]);
+          acc[2 * q + 1] = fmaf(w[0], hi * down, acc[2 * q + 1]);
         }
       }
     }
@@ -2036,7 +2024,6 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
 
   CombineArgs ca{};
   ca.y = y;
-  ca.y_f32 = p.y_f32;
   ca.yexp = reinterpret_cast<const uint8_t*>(base + p.yexp_off);
   ca.P = (int)p.P;
   ca.place = reinterpret_cast<const int*>(base + p.place_off);
@@ -2047,7 +2034,9 @@ int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall& c, void* workspa
   ca.topk = (int)p.topk;
   ca.out_f32 = c.out_f32;
   const int64_t n = (p.T * (p.H / 8) + 255) / 256;
-  hipLaunchKernelGGL(experts_combine_kernel, dim3((unsigned)(n > 16384 ? 16384 : n)), dim3(256), 0, s, ca);
+  const dim3 cgrid((unsigned)(n > 16384 ? 16384 : n));
+  if (p.y_f32) hipLaunchKernelGGL(experts_combine_kernel<true>, cgrid, dim3(256), 0, s, ca);
+  else hipLaunchKernelGGL(experts_combine_kernel<false>, cgrid, dim3(256), 0, s, ca);
   return (int)hipGetLastError();
 }
 
