@@ -407,3 +407,19 @@ def test_whole_block_in_a_graph(T):
         for a, b in zip(got, (d["ids"], d["weights"], out, y)):
             assert torch.equal(a, b)
     check_experts(d, out)
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_example_block(tokens, capsys):
+    """The example's block: roundings of bf16 between its calls, and 8-bit flips behind them
+    (each bf16 rounding before a quantisation moves values across an e4m3 midpoint now and
+    then; a few percent of a value's spacing, in the 2-norm well under 2e-2)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    off = module.main(["--tokens", str(tokens), "--hidden", "512", "--inter", "256", "--experts", "8", "--topk", "2",
+                       "--latent", "132", "--steps", "2"])
+    assert off < 2e-2
