@@ -1341,13 +1341,15 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
           make_rsrc(static_cast<uint8_t*>(g.out) + (size_t)cur.start * g.N, (uint32_t)cur.count * (uint32_t)g.N);
       const __amdgpu_buffer_rsrc_t sr =
           make_rsrc(g.hs + (size_t)(cur.f0 / 128) * g.hs_ld + cur.start, (uint32_t)cur.count * 4u);
-      static_assert(TM % 4 == 0, "four row tiles' scales per store");
 #pragma unroll
       for (int i = 0; i < TM; i += 4) {
         // Lane group q stores the scales of row tile i + q (the first wave column's lanes).
-        const float t4 = lg == 0 ? top[i] : lg == 1 ? top[i + 1] : lg == 2 ? top[i + 2] : top[i + 3];
+        float t4 = top[i];
+#pragma unroll
+        for (int q = 1; q < 4; ++q)
+          if (i + q < TM && lg == q) t4 = top[i + q];
         const uint32_t r = (uint32_t)((wm * TM + i + lg) * 16 + ln);
-        buf_st4(sr, wn == 0 ? r * 4u : kNoRow, __float_as_uint(t4 / kE4M3Max));
+        buf_st4(sr, wn == 0 && i + lg < TM ? r * 4u : kNoRow, __float_as_uint(t4 / kE4M3Max));
       }
       constexpr int HB = 16 * FT;  // bytes of a row: two 16-byte chunks (FT == 2)
       static_assert(FT == 2 && TM % 2 == 0, "two row tiles per store");
@@ -1371,7 +1373,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
         buf_st16(hr, n < g.N ? r * (uint32_t)g.N + (uint32_t)n : kNoRow, v);
         __builtin_amdgcn_wave_barrier();
       }
-      stores = TM / 4 + TM / 2;
+      stores = (TM + 3) / 4 + TM / 2;
     } else {
       constexpr int CPR = 2 * TN, RPI = 64 / CPR;  // 16-byte chunks per staged row, rows per store
       const bool whole = MODE == F8_DOWN
@@ -1426,11 +1428,14 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
               g.yexp + (size_t)(cur.f0 / 64 + wn) * g.hs_ld + cur.start, cur.f0 + wn * 64 < g.N ? (uint32_t)cur.count : 0u);
 #pragma unroll
           for (int i = 0; i < TM; i += 4) {
-            const uint32_t e4 = lg == 0 ? ex[i] : lg == 1 ? ex[i + 1] : lg == 2 ? ex[i + 2] : ex[i + 3];
-            buf_st1(er, (uint32_t)((wm * TM + i + lg) * 16 + ln), e4);
+            uint32_t e4 = ex[i];
+#pragma unroll
+            for (int q = 1; q < 4; ++q)
+              if (i + q < TM && lg == q) e4 = ex[i + q];
+            buf_st1(er, i + lg < TM ? (uint32_t)((wm * TM + i + lg) * 16 + ln) : kNoRow, e4);
           }
         }
-        stores = TM * (16 / RPI) + (MODE == F8_DOWN ? TM / 4 : 0);
+        stores = TM * (16 / RPI) + (MODE == F8_DOWN ? (TM + 3) / 4 : 0);
       } else {
         stores = -1;
 #pragma unroll
@@ -1449,7 +1454,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
     }
     if (!more) break;
     constexpr int CPRW = 2 * TN;
-    constexpr int FIXED = GU ? TM / 4 + TM / 2 : TM * (16 * CPRW / 64) + (MODE == F8_DOWN ? TM / 4 : 0);
+    constexpr int FIXED = GU ? (TM + 3) / 4 + TM / 2 : TM * (16 * CPRW / 64) + (MODE == F8_DOWN ? (TM + 3) / 4 : 0);
     static_assert(AHEAD + FIXED < 64, "vmcnt range");
     if (stores == FIXED) wait_vmcnt<AHEAD + FIXED>();
     else wait_vmcnt<0>();
@@ -1771,7 +1776,7 @@ int launch_f8(const F8Plan& p, const F8Args& a, int max_tiles, hipStream_t s) {
                          dim3(WM_ * WN_ * 64), 0, s, g);                                               \
     return (int)hipGetLastError();                                                                     \
   }
-  SMLP_F8(64, 256, 1, 4, 3) SMLP_F8(256, 256, 2, 4, 2)
+  SMLP_F8(64, 256, 2, 4, 3) SMLP_F8(256, 256, 2, 4, 2)
   if constexpr (MODE == F8_LINEAR) { SMLP_F8(64, 64, 2, 2, 4) SMLP_F8(128, 128, 2, 2, 2) }
 #undef SMLP_F8
   return (int)hipErrorInvalidConfiguration;
