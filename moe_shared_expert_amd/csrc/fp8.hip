@@ -101,16 +101,6 @@ __device__ __forceinline__ void f8_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int LPS, int MAXL>
-__device__ __forceinline__ void f8_wait_steps(int later) {
-  if constexpr (MAXL == 0) {
-    wait_vmcnt<0>();
-  } else {
-    if (later >= MAXL) wait_vmcnt<MAXL * LPS>();
-    else f8_wait_steps<LPS, MAXL - 1>(later);
-  }
-}
-
 // Store four consecutive features n .. n+3 of one output row.
 __device__ __forceinline__ void f8_store4(const F8Args& g, size_t row, int n, f32x4 v) {
   const size_t at = row * (size_t)g.ldo + n;
@@ -171,7 +161,10 @@ __device__ __forceinline__ i32x8 act_frag(const char* tile, int row, int lg) {
   return v;
 }
 
-// Weight streaming (few rows per tile).  A workgroup owns NT tiles of 16 weight rows
+// Weight streaming (few rows per tile), bound by HBM: the gate_up of 32 tokens of 8 pairs over
+// 128 experts (H = 7168, I = 768) reads its 95 or so experts' 1.05 GB in 164 us, 6.4 TB/s.
+// Tiles of 8 rows instead of 16 and three ring stages instead of four let a second workgroup
+// live on a compute unit (180 -> 164 us).  A workgroup owns NT tiles of 16 weight rows
 // (gate_up: NT / 2 tiles of gate rows and the matching up rows) and one tile of 8 * AH
 // activation rows; its waves take the K blocks in turn, each through a ring of its own, and
 // their sums are added in wave order.
@@ -325,7 +318,10 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
 // Most 128-row blocks that a run of the short-K down kernel touches.
 constexpr int kDownBlocks = kDownRun / 8 + 2;
 
-// Down product of few rows per expert and a short K (KB <= KBMAX blocks).  A workgroup holds
+// Down product of few rows per expert and a short K (KB <= KBMAX blocks), bound by HBM: the
+// same experts' 0.52 GB in 97 us, 5.4 TB/s; with K split over the waves as above, six blocks
+// left each wave one or two steps and the time was in starting and ending workgroups (221 us).
+// A workgroup holds
 // its tile's activations (h in fp32, brought to the 8-bit form here) in LDS and streams a run
 // of `run` 16-row weight tiles; its waves take the tiles in turn, each wave with the whole K
 // and a ring of D blocks of 16 rows x 128 bytes that runs on from tile to tile.
@@ -458,7 +454,7 @@ __global__ __launch_bounds__(256) void f8_down_kernel(F8Args g, const float* h, 
 // turn, D blocks of loads in flight, and their sums are added in wave order.  The work on x
 // (about 200 instructions a block, for every workgroup anew) bounds a workgroup, so with few
 // weight rows K is split over workgroups too (gridDim.y); the last one to arrive at a counter
-// adds the slices in order.
+// adds the slices in order (16 x 132 x 7168: 13.4 us on nine workgroups, 6.2 us on 63).
 struct NarrowArgs {
   const void* x;   // [M, K] bf16
   const uint8_t* w;
@@ -602,7 +598,9 @@ __global__ __launch_bounds__(512, 2) void f8_narrow_kernel(NarrowArgs a) {
 
 // ---- one activation row ----
 // A single row leaves the matrix instructions with one column in sixteen, so these kernels
-// multiply in the vector unit, straight from registers: a 16-byte load per lane covers 8
+// multiply in the vector unit, straight from registers (one token of 8 experts, H = 7168, I =
+// 768: gate_up 88 MB in 16.7 us, 5.3 TB/s; down 44 MB in 12.2 us; a projection of 2112 x 7168
+// 7.0 us, mostly latency): a 16-byte load per lane covers 8
 // weight rows x 128 bytes (8 whole lines), lane l holding 16 K elements of row l / 8, and
 // each lane keeps NB such loads in flight.  The row of x sits in LDS in its 8-bit form.
 
@@ -930,6 +928,14 @@ __device__ __forceinline__ void buf_st1(__amdgpu_buffer_rsrc_t r, uint32_t off, 
 // LDS-tiled kernel: BM activation rows x BN weight rows (gate_up: BN / 2 features and
 // both their rows) per tile, WM x WN waves; a workgroup takes tiles lin, lin + gridDim.x, ...
 // EXACT: products through bf16.
+//
+// 8192 x 7168 x 6144 in 322 us, 2.24 PFLOP/s (torch's library product with one scale for a
+// whole tensor 299 us): the matrix cores are busy 53% of the time at 2.0 GHz; of the rest, half
+// a round of tiles (896 over 256 compute units) is 12%, and without the loads or without the
+// scaling's multiply-adds, which share the issue slots, the kernel would take 292 or 297 us.
+// gate_up of 65536 pairs (I = 768) 700 us, 2.1 PFLOP/s with an eighth of the rows empty; down
+// 530 us, 1.36 PFLOP/s: six blocks of K per tile against 128 KB of results, whose stores the
+// next tile's second step has to wait for.
 template <int BM, int BN, int WM, int WN, int NS, int MODE, bool EXACT>
 __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
   constexpr bool GU = MODE == F8_GATE_UP;
@@ -1464,7 +1470,8 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
 }
 
 // Quantisation of rows in groups of 128 columns: 16 lanes per group, 8 elements each.
-// scale of row r, group b: s[r * s_row + b * s_kb].
+// scale of row r, group b: s[r * s_row + b * s_kb].  Bound by HBM: 8192 x 6144 bf16 in 33 us,
+// 4.6 TB/s read and written.
 struct QuantArgs {
   const void* x;
   int64_t rows;
@@ -1776,7 +1783,8 @@ int launch_f8(const F8Plan& p, const F8Args& a, int max_tiles, hipStream_t s) {
                          dim3(WM_ * WN_ * 64), 0, s, g);                                               \
     return (int)hipGetLastError();                                                                     \
   }
-  SMLP_F8(64, 256, 2, 4, 3) SMLP_F8(256, 256, 2, 4, 2)
+  SMLP_F8(256, 256, 2, 4, 2)
+  if constexpr (MODE != F8_LINEAR) { SMLP_F8(64, 256, 2, 4, 3) }
   if constexpr (MODE == F8_LINEAR) { SMLP_F8(64, 64, 2, 2, 4) SMLP_F8(128, 128, 2, 2, 2) }
 #undef SMLP_F8
   return (int)hipErrorInvalidConfiguration;

@@ -165,6 +165,8 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
   const int64_t HB = blocks128(H), IB = blocks128(I);
   const int64_t active = p.P < E ? p.P : E;
   const int64_t rows = active ? p.P / active : 0;
+  // Streaming against tiles of 64 rows, the same experts: 8 rows per expert 198 and 235 us, 16
+  // rows 265 and 241 us.
   if (rows <= 12) {
     p.gu = stream_plan(rows * 2, HB);
     p.dn = stream_plan(rows * 2, IB);
@@ -177,7 +179,9 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
       p.dn.run = (int)(run < 4 ? 4 : run > smlp::kDownRun ? smlp::kDownRun : (run + 3) / 4 * 4);
     }
   } else {
-    const int bm = rows >= 192 ? 256 : 64;
+    // 8 of 64 experts of 768, H = 7168: 96 rows per expert take 369 us on tiles of 256 rows and
+    // 376 us on tiles of 64, 128 rows 390 and 416 us, 64 rows 343 and 303 us.
+    const int bm = rows >= 112 ? 256 : 64;
     p.gu = tile_plan(bm, 256, HB, partial_fp32 != 0);
     p.dn = tile_plan(bm, 256, IB, partial_fp32 != 0);
   }
