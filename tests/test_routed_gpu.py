@@ -423,3 +423,39 @@ def test_example_block(tokens, capsys):
     off = module.main(["--tokens", str(tokens), "--hidden", "512", "--inter", "256", "--experts", "8", "--topk", "2",
                        "--latent", "132", "--steps", "2"])
     assert off < 2e-2
+
+
+# ------------------------------------------------------------------ several tiles per workgroup
+
+@pytest.mark.parametrize("out_fp32", [False, True])
+@pytest.mark.parametrize("size", [(8192, 2300, 1280), (3000, 3001, 1040), (1900, 1890, 2048)])
+def test_linear_of_many_tiles(size, out_fp32):
+    """More tiles than workgroups (of 256, 128 and 64 rows).  fp32 sums as above; with bf16
+    results the 8-bit instruction may be 1.8e-5 of a block's absolute products off."""
+    M, K, N = size[0], size[2], size[1]
+    g = torch.Generator(device=DEV).manual_seed(M)
+    x, xs = binding.quantize_fp8(torch.randn(M, K, generator=g, device=DEV))
+    w, ws = binding.quantize_fp8(torch.randn(N, K, generator=g, device=DEV), 128)
+    x64 = x.double() * xs.double().repeat_interleave(128, 1)[:, :K]
+    w64 = w.double() * ws.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    ref, size_ = x64 @ w64.t(), x64.abs() @ w64.abs().t()
+    y = binding.linear_fp8(x, w, ws, xs, out_fp32).double()
+    n = 132 + routed.blocks(K)
+    tol = n * U * size_ if out_fp32 else (1.8e-5 + n * U) * size_ + 2.0 ** -8 * ref.abs()
+    assert bool(((y - ref).abs() <= tol).all())
+
+
+def test_experts_of_many_tiles():
+    """More row tiles than workgroups in both products: the same rows as in small calls, up to
+    flips of h (a tile out of place would be off by the whole of its rows)."""
+    T, H, I, E, k = 4096, 2048, 1152, 4, 2
+    d = make_experts(6, T, H, I, E, k)
+    for partial in (False, True):
+        whole = run_experts(d, partial=partial).double()
+        for t0 in range(0, T, 256):
+            part = dict(d)
+            for n in ("x", "ids", "weights"):
+                part[n] = d[n][t0:t0 + 256].contiguous()
+            small = run_experts(part, partial=partial).double()
+            off = (whole[t0:t0 + 256] - small).norm(dim=1) / small.norm(dim=1)
+            assert off.max() < 2e-2, (partial, t0, off.max())
