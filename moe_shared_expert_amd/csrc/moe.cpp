@@ -211,7 +211,9 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
   p.xs_off = take((size_t)(T * HB) * 4);
   p.h8_off = take((size_t)(p.P * I));
   p.hs_off = take((size_t)(p.P * IB) * 4);
-  p.h32_off = take(stream ? (size_t)(p.P * I) * 4 : 0);
+  // fp32 h: the streaming gate_up, and the two launches of one token whatever p.gu says (many
+  // choices among few experts make p.gu tiled).
+  p.h32_off = take(stream || p.token ? (size_t)(p.P * I) * 4 : 0);
   p.y_off = take((size_t)p.P * (size_t)H * (p.y_f32 ? 4 : 2));
   p.workspace_bytes = off;
   *out = p;

@@ -1,0 +1,109 @@
+// Drives csrc/moe.cpp with launchers that look at the plans they are handed: every part of
+// the workspace that a launch reads or writes lies inside the size that was asked for and
+// apart from the others.  Host only, built with sanitizers.
+#include <algorithm>
+#include <cstdio>
+#include <string>
+#include <utility>
+#include <vector>
+
+#include "internal.h"
+#include "smlp.h"
+
+static std::string g_detail;
+static int g_bad = 0, g_launches = 0;
+static char g_case[256];
+
+static void require(bool ok, const char* what) {
+  if (ok) return;
+  if (g_bad++ < 20) std::printf("%s: %s\n", g_case, what);
+}
+
+static int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+
+namespace smlp {
+int set_error(int status, const char* detail) {
+  g_detail = detail;
+  return status;
+}
+int launch_route(const void*, int, int64_t, int64_t, int64_t, const float*, const smlp_route&, int32_t*, float*,
+                 hipStream_t) {
+  return 0;
+}
+int launch_quant_fp8(const void*, int, int64_t, int64_t, int64_t, int64_t, int, void*, float*, int64_t, int64_t,
+                     hipStream_t) {
+  return 0;
+}
+int launch_row_fp8(const void*, const float*, const void*, const float*, void*, int64_t, int64_t, int, hipStream_t) {
+  return 0;
+}
+int launch_narrow_fp8(const F8Plan&, const void*, const void*, const float*, void*, int64_t, int64_t, int64_t, int64_t,
+                      int, float*, hipStream_t) {
+  return 0;
+}
+int launch_linear_fp8(const F8Plan&, const void*, const float*, int64_t, int64_t, const void*, const float*, void*,
+                      int64_t, int64_t, int64_t, int64_t, int, float*, hipStream_t) {
+  return 0;
+}
+
+int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall&, void*, hipStream_t) {
+  ++g_launches;
+  const int64_t HB = blocks128(p.H), IB = blocks128(p.I);
+  std::vector<std::pair<size_t, size_t>> used;  // offset, bytes
+  auto use = [&](size_t off, int64_t bytes) { used.push_back({off, (size_t)bytes}); };
+  if (p.token) {
+    use(p.h32_off, p.topk * p.I * 4);
+  } else {
+    const bool stream = p.gu.kind == F8_KIND_STREAM, short_k = p.dn.kind == F8_KIND_DOWN;
+    use(p.hdr_off, (4 + 4 * p.max_tiles) * 4);
+    use(p.perm_off, p.P * 4);
+    use(p.place_off, p.P * 4);
+    if (p.chunk) use(p.counts_off, (p.P + p.chunk - 1) / p.chunk * p.E * 4);
+    use(p.x8_off, p.T * p.H);
+    use(p.xs_off, p.T * HB * 4);
+    if (stream) use(p.h32_off, p.P * p.I * 4);
+    if (!short_k) {
+      use(p.h8_off, p.P * p.I);
+      use(p.hs_off, p.P * IB * 4);
+    }
+    use(p.y_off, p.P * p.H * (p.y_f32 ? 4 : 2));
+    if (!p.y_f32) use(p.yexp_off, p.P * ((p.H + 63) / 64));
+  }
+  std::sort(used.begin(), used.end());
+  size_t end = 0;
+  for (const auto& u : used) {
+    require(u.first % 256 == 0, "a region is not aligned");
+    require(u.first >= end, "regions overlap");
+    end = u.first + u.second;
+  }
+  require(end <= p.workspace_bytes, "a region ends behind the workspace");
+  return 0;
+}
+}  // namespace smlp
+
+static char* at(uintptr_t v) { return reinterpret_cast<char*>(v << 40); }
+static float* fat(uintptr_t v) { return reinterpret_cast<float*>(at(v)); }
+
+static void experts_regions() {
+  const int64_t sizes[][2] = {{256, 512}, {512, 256}, {16, 2048}, {128, 4096}, {8208, 128}, {2000, 336}, {7168, 768}};
+  for (int64_t T : {1, 2, 5, 40, 301, 600, 5000})
+    for (int64_t E : {1, 2, 3, 24, 128})
+      for (int64_t topk : {1, 2, 4, 8, 12, 13, 25, 26, 39, 64})
+        for (const auto& s : sizes)
+          for (int partial : {0, 1}) {
+            std::snprintf(g_case, sizeof g_case, "T %lld H %lld I %lld E %lld topk %lld partial %d", (long long)T,
+                          (long long)s[0], (long long)s[1], (long long)E, (long long)topk, partial);
+            size_t n = 0;
+            if (shared_mlp_experts_fp8_workspace_bytes(T, s[0], s[1], E, topk, partial, &n)) continue;
+            g_launches = 0;
+            const int rc = shared_mlp_experts_fp8(at(1), reinterpret_cast<int32_t*>(at(2)), fat(3), at(4), fat(5), at(6),
+                                                  fat(7), at(8), T, s[0], s[1], E, topk, 0, partial, at(9), n, nullptr);
+            require(rc == SMLP_OK && g_launches == 1, g_detail.c_str());
+          }
+}
+
+int main() {
+  experts_regions();
+  std::printf(g_bad ? "%d checks failed\n" : "all checks passed\n", g_bad);
+  return g_bad != 0;
+}

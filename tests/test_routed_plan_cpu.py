@@ -1,0 +1,30 @@
+"""Host-only tests of the routed half's plans and binding: what the launchers are handed, and
+what the Python entry points do around a call.  No GPU."""
+import os
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+from conftest import ROOT
+
+binding = pytest.importorskip("moe_shared_expert_amd.binding")
+
+
+def test_plans_stay_inside_the_workspace(tmp_path):
+    gxx = shutil.which("g++")
+    if gxx is None or not os.path.exists("/opt/rocm/include/hip/hip_runtime.h"):
+        pytest.skip("needs g++ and the ROCm headers")
+    exe = str(tmp_path / "routed_plans")
+    csrc = os.path.join(ROOT, "moe_shared_expert_amd", "csrc")
+    cmd = [gxx, "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined",
+           "-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include", "-I", os.path.join(ROOT, "include"), "-I", csrc,
+           os.path.join(csrc, "moe.cpp"), os.path.join(ROOT, "tests", "sanitize", "routed_plan_driver.cpp"), "-o", exe,
+           "-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib", "-pthread"]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-4000:]
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=0:halt_on_error=1",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=600, env=env)
+    assert r.returncode == 0 and "all checks passed" in r.stdout, (r.stdout + r.stderr)[-4000:]
