@@ -51,6 +51,7 @@ struct F8Args {
   int ldo;
   int out_f32;         // fp32 (1) or bf16 (0) output; gate_up: fp32 h (1) or e4m3 h (0); down:
                        // fp32 y (1) or fp16 y with exponents (0)
+  int by_rows;         // tiled projection with bf16 y: full tiles store whole rows through a buffer
   float* hs;           // gate_up with e4m3 h: scales, block b of position p at hs[b * hs_ld + p]
   int hs_ld;
   uint8_t* yexp;       // down with fp16 y: exponent of position p and columns 64 c .. + 63 at
@@ -89,8 +90,10 @@ __device__ __forceinline__ int f8_arow(const F8Args& g, int mode, int start, int
 }
 
 // Byte offsets that make a buffer load return zeros: kNoRow in place of a row's offset,
-// kNoChunk added to one.  Buffers hold at most 2^31 - 16 bytes, so a real offset plus
-// kNoChunk, and kNoRow plus any, is out of range, and nothing wraps.
+// kNoChunk added to one.  Operands hold at most 2^31 - 16 bytes, so a real offset plus
+// kNoChunk, and kNoRow plus any, is out of range, and nothing wraps.  kNoRow also drops a
+// store: results that are stored through a buffer are held to the same size (the planner's
+// rows_fit_buffer; h of a tile is less than 2^31 bytes because h of all pairs is).
 constexpr uint32_t kNoRow = 0x80000000u, kNoChunk = 0x7ffffff0u;
 
 __device__ __forceinline__ void f8_barrier() {
@@ -1376,15 +1379,14 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
         const u32x4 v{from[0], from[1], from[2], from[3]};
         const uint32_t r = (uint32_t)((wm * TM + i) * 16 + rr);
         const int n = cur.f0 + wn * HB + c * 16;  // N is a multiple of 16
-        buf_st16(hr, n < g.N ? r * (uint32_t)g.N + (uint32_t)n : kNoRow, v);
+        // Rows past the tile's are dropped here: with a wide N their offsets would wrap.
+        buf_st16(hr, n < g.N && (int)r < cur.count ? r * (uint32_t)g.N + (uint32_t)n : kNoRow, v);
         __builtin_amdgcn_wave_barrier();
       }
       stores = (TM + 3) / 4 + TM / 2;
     } else {
       constexpr int CPR = 2 * TN, RPI = 64 / CPR;  // 16-byte chunks per staged row, rows per store
-      const bool whole = MODE == F8_DOWN
-                             ? !g.out_f32
-                             : !g.out_f32 && cur.f0 + FN <= g.N && g.ldo % 8 == 0 && ((uintptr_t)g.out & 15) == 0;
+      const bool whole = MODE == F8_DOWN ? !g.out_f32 : g.by_rows && cur.f0 + FN <= g.N;
       if (whole) {
         // Rows through LDS: a lane's four features are 8 bytes of 16 different rows, the
         // stores below whole runs of 32 TN bytes per row.  Projection: bf16.  Experts: fp16
@@ -1877,6 +1879,7 @@ int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t 
   g.out = y;
   g.ldo = (int)ldy;
   g.out_f32 = out_f32;
+  g.by_rows = p.by_rows && !out_f32 && ldy % 8 == 0 && (uintptr_t)y % 16 == 0;
   g.part = part;
   const int tiles = (int)((M + p.bm - 1) / p.bm);
   F8Plan q = p;

@@ -149,6 +149,12 @@ constexpr int kOneSort = 4096, kSortChunks = 64;
 // Most K slices of a projection, and most tiles (columns of workgroups) with a K split.
 constexpr int kSlices = 8, kReduceTiles = 256;
 
+// Whether `rows` rows of n 2-byte elements, ld apart, fit a buffer resource whose stores can be
+// dropped: an offset of 2^31 has to be past its end, so it spans at most 2^31 - 16 bytes.
+constexpr bool rows_fit_buffer(int64_t rows, int64_t ld, int64_t n) {
+  return ((rows - 1) * ld + n) * 2 <= ((int64_t)1 << 31) - 16;
+}
+
 // One 8-bit block-scaled product (fp8.hip).
 enum { F8_KIND_STREAM = 0, F8_KIND_TILE = 1, F8_KIND_DOWN = 2, F8_KIND_ROW = 3, F8_KIND_NARROW = 4 };
 struct F8Plan {
@@ -158,6 +164,7 @@ struct F8Plan {
   int run;                    // short-K down: 16-row weight tiles per workgroup
   int bn;                     // tiled: weight rows per workgroup
   int exact;                  // tiled: products through bf16 (fp32 results)
+  int by_rows;                // tiled projection: a tile's rows of y fit one buffer (rows_fit_buffer)
   int ksplit, kslice;         // tiled projection: K slices over workgroups, 128-element blocks per slice
 };
 

@@ -190,6 +190,8 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
   // fp32 rows of y as long as they stay in the caches (301 tokens of 4 pairs of 2000: weighted
   // sum 4.0 us against 5.7 us from fp16 rows).
   p.y_f32 = stream || partial_fp32 || p.P * H <= (4 << 20);
+  // fp16 rows are stored through a buffer per tile; rows too long for that stay fp32.
+  if (!p.y_f32 && !smlp::rows_fit_buffer(p.P < p.dn.bm ? p.P : p.dn.bm, H, H)) p.y_f32 = 1;
   // An expert with c rows needs ceil(c / bm) tiles.
   p.max_tiles = p.P / p.gu.bm + active;
   size_t off = 0;
@@ -317,6 +319,7 @@ int shared_mlp_linear_fp8(const void* x, const float* x_scales, const void* w, c
   if (rc) return rc;
   if (ldy < N || !fits(M, ldy)) return fail(SMLP_ERR_SHAPE, "ldy = %lld is below N or M * ldy not below 2^31", (long long)ldy);
   if (M == 0) return ok();
+  p.f.by_rows = smlp::rows_fit_buffer(M < p.f.bm ? M : p.f.bm, ldy, N);
   const size_t oe = out_fp32 ? 4 : 2;
   if ((rc = check_ptr(x, "x", 16)) || (rc = check_ptr(w, "w", 16)) || (rc = check_ptr(w_scales, "w_scales", 4)) ||
       (rc = check_ptr(y, "y", oe)))

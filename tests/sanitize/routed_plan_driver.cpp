@@ -41,14 +41,21 @@ int launch_narrow_fp8(const F8Plan&, const void*, const void*, const float*, voi
                       int, float*, hipStream_t) {
   return 0;
 }
-int launch_linear_fp8(const F8Plan&, const void*, const float*, int64_t, int64_t, const void*, const float*, void*,
-                      int64_t, int64_t, int64_t, int64_t, int, float*, hipStream_t) {
+// Dropped stores are aimed at byte 2^31 of a tile's results, which therefore end before it.
+static bool drops(int64_t rows, int64_t ld, int64_t n) { return ((rows - 1) * ld + n) * 2 <= 0x7ffffff0; }
+
+int launch_linear_fp8(const F8Plan& p, const void*, const float*, int64_t, int64_t, const void*, const float*, void*,
+                      int64_t M, int64_t, int64_t N, int64_t ldy, int, float*, hipStream_t) {
+  ++g_launches;
+  if (p.kind == F8_KIND_TILE) require(!p.by_rows == !drops(M < p.bm ? M : p.bm, ldy, N), "by_rows");
   return 0;
 }
 
 int launch_experts_fp8(const ExpertsPlan& p, const ExpertsCall&, void*, hipStream_t) {
   ++g_launches;
   const int64_t HB = blocks128(p.H), IB = blocks128(p.I);
+  if (!p.token && !p.y_f32)
+    require(drops(p.P < p.dn.bm ? p.P : p.dn.bm, p.H, p.H), "dropped stores of y would land in it");
   std::vector<std::pair<size_t, size_t>> used;  // offset, bytes
   auto use = [&](size_t off, int64_t bytes) { used.push_back({off, (size_t)bytes}); };
   if (p.token) {
@@ -85,8 +92,10 @@ static char* at(uintptr_t v) { return reinterpret_cast<char*>(v << 40); }
 static float* fat(uintptr_t v) { return reinterpret_cast<float*>(at(v)); }
 
 static void experts_regions() {
-  const int64_t sizes[][2] = {{256, 512}, {512, 256}, {16, 2048}, {128, 4096}, {8208, 128}, {2000, 336}, {7168, 768}};
-  for (int64_t T : {1, 2, 5, 40, 301, 600, 5000})
+  const int64_t sizes[][2] = {{256, 512},   {512, 256},    {16, 2048},     {128, 4096},    {8208, 128},
+                              {2000, 336},  {7168, 768},   {4194304, 128}, {8388608, 112}, {18000016, 16},
+                              {33554432, 16}};
+  for (int64_t T : {1, 2, 5, 40, 62, 127, 255, 301, 600, 5000})
     for (int64_t E : {1, 2, 3, 24, 128})
       for (int64_t topk : {1, 2, 4, 8, 12, 13, 25, 26, 39, 64})
         for (const auto& s : sizes)
@@ -102,8 +111,24 @@ static void experts_regions() {
           }
 }
 
+static void linear_rows() {
+  const int64_t cases[][4] = {  // M, K, N, ldy
+      {200, 128, 6000000, 6000000}, {200, 128, 5000000, 5000000}, {60, 128, 64, 35000000},  {60, 128, 64, 17000000},
+      {1000, 256, 4096, 2000000},   {8192, 6144, 7168, 7168},     {300, 256, 1024, 7000000}, {63, 1024, 64, 17300000}};
+  for (const auto& c : cases)
+    for (int f32 : {0, 1}) {
+      std::snprintf(g_case, sizeof g_case, "M %lld K %lld N %lld ldy %lld fp32 %d", (long long)c[0], (long long)c[1],
+                    (long long)c[2], (long long)c[3], f32);
+      g_launches = 0;
+      const int rc = shared_mlp_linear_fp8(at(1), fat(2), at(3), fat(4), at(5), c[0], c[1], c[2], c[3], f32, at(6),
+                                           (size_t)1 << 39, nullptr);
+      require(rc == SMLP_OK && g_launches == 1, g_detail.c_str());
+    }
+}
+
 int main() {
   experts_regions();
+  linear_rows();
   std::printf(g_bad ? "%d checks failed\n" : "all checks passed\n", g_bad);
   return g_bad != 0;
 }

@@ -32,3 +32,99 @@ def test_one_token_of_many_choices_among_few_experts(size, partial):
                                    workspace=buf[:need])
     assert bool((buf[need:] == 0xA5).all())
     check_experts(d, out)
+
+
+# ------------------------------------------------------------------ offsets past 31 bits
+
+def product_within(y, x, xs, w, ws, K, out_fp32=False):
+    """y [M, n] against the product in fp64 (K <= 512: exact products, fp32 sums)."""
+    x64 = x.double() * xs.double().repeat_interleave(128, 1)[:, :K]
+    w64 = w.double() * ws[:, :, None, None].double().expand(-1, -1, 128, 128).permute(0, 2, 1, 3).reshape(
+        ws.shape[0] * 128, -1)[:w.shape[0], :K]
+    ref, size = x64 @ w64.t().contiguous(), x64.abs() @ w64.abs().t().contiguous()
+    tol = (128 + routed.blocks(K) + 4) * U * size + (0 if out_fp32 else 2.0 ** -8 * ref.abs())
+    return bool(((y.double() - ref).abs() <= tol).all())
+
+
+def test_linear_result_past_2_31_bytes():
+    """A tile of 200 rows whose 256-row frame ends behind byte 2^31 of y: the frame's missing
+    rows are dropped, not stored there (row 178 from column 5741824 on)."""
+    M, K, N = 200, 128, 6_000_000
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x, xs = binding.quantize_fp8(torch.randn(M, K, generator=g, device=DEV).bfloat16())
+    w, ws = binding.quantize_fp8(torch.randn(N, K, generator=g, device=DEV, dtype=torch.bfloat16), 128)
+    y = binding.linear_fp8(x, w, ws, xs)
+    at = (1 << 30) - 178 * N
+    for c0 in (0, at - at % 128, 128 * 20000, N // 128 * 128 - 4096):
+        c1 = min(N, c0 + 16384)
+        assert product_within(y[:, c0:c1], x, xs, w[c0:c1], ws[c0 // 128:-(-c1 // 128)], K), c0
+
+
+def test_linear_rows_far_apart():
+    M, K, N, ldy = 60, 128, 64, 35_000_000
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x, xs = binding.quantize_fp8(torch.randn(M, K, generator=g, device=DEV).bfloat16())
+    w, ws = binding.quantize_fp8(torch.randn(N, K, generator=g, device=DEV), 128)
+    y = torch.full((M, ldy), 3.0, dtype=torch.bfloat16, device=DEV)
+    binding.shared_mlp_linear_fp8(x, w, ws, y[:, :N], xs)
+    assert product_within(y[:, :N], x, xs, w, ws, K)
+    assert bool((y[:, N:] == 3.0).all())
+
+
+def check_columns(d, out, wgu64, cols, hcols):
+    """Columns `cols` of out, one expert and one choice per token; h's columns `hcols` (whole
+    groups) are the only ones with a weight in w_down."""
+    q, s = routed.quantize(d["x"].float().cpu().numpy())
+    x64 = routed.dequantize(q, s)
+    I = hcols.numel()
+    wd = f64(d["qd"][0][:, hcols][cols]) * f64(d["sd"][0][cols // 128][:, hcols // 128])
+    gu = x64 @ wgu64.T
+    hq, hs = routed.quantize((gu[:, :I] / (1.0 + np.exp(-gu[:, :I])) * gu[:, I:]).astype(np.float32))
+    h = routed.dequantize(hq, hs)
+    w = f64(d["weights"])
+    ref, size = w * (h @ wd.T), w * (np.abs(h) @ np.abs(wd).T)
+    step = np.maximum(np.abs(h) / 8.0, np.repeat(hs.astype(np.float64), 128, 1)[:, :I] * 2.0 ** -9)
+    flip = np.stack([w[t] * (np.abs(wd) * step[t]).max(axis=1) for t in range(h.shape[0])])
+    tol = (128 + routed.blocks(I) + 9) * U * size + 2 * flip + 2.0 ** -8 * 2.01 * np.abs(ref) + 1e-30
+    err = np.abs(f64(out[:, cols]) - ref)
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+def test_experts_wide_rows():
+    """62 rows of y of one expert end behind byte 2^31.  x is zero past its first block, so the
+    sums over 18 million elements stay exact."""
+    T, H, I = 62, 18_000_016, 16
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    x[:, :128] = torch.randn(T, 128, generator=g, device=DEV)
+    qgu, sgu = binding.quantize_fp8(torch.randn(2, I, H, generator=g, device=DEV, dtype=torch.bfloat16), 128)
+    qd, sd = binding.quantize_fp8(torch.randn(1, H, I, generator=g, device=DEV, dtype=torch.bfloat16), 128)
+    d = dict(x=x, ids=torch.zeros(T, 1, dtype=torch.int32, device=DEV),
+             weights=torch.rand(T, 1, generator=g, device=DEV), qgu=qgu.view(1, 2 * I, H),
+             sgu=sgu.view(1, 2, -1), qd=qd, sd=sd)
+    out = binding.experts_fp8(x, d["ids"], d["weights"], d["qgu"], d["sgu"], qd, sd)
+    wgu = torch.cat([qgu[p, :, :128].double() * sgu[p, 0, 0].double() for p in (0, 1)]).cpu().numpy()
+    at = (1 << 30) - 59 * H
+    cols = torch.cat([torch.arange(c, c + 512) for c in (0, at, H - 512)]).to(DEV)
+    x128 = dict(d, x=x[:, :128])
+    check_columns(x128, out, wgu, cols, torch.arange(I, device=DEV))
+
+
+def test_experts_wide_intermediate():
+    """112 rows of h on a frame of 256 rows of 18 million: offsets of the missing rows pass 32
+    bits.  w_down is zero except for the columns that wrapped offsets would reach, so the sums
+    stay exact."""
+    T, H, I = 112, 16, 18_000_000
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.randn(T, H, generator=g, device=DEV).bfloat16()
+    qgu, sgu = binding.quantize_fp8(torch.randn(2, I, H, generator=g, device=DEV, dtype=torch.bfloat16), 128)
+    hcols = torch.cat([torch.arange(c, c + 128) for c in (0, 7_040_000, 14_080_000, I - 128)]).to(DEV)
+    wd = torch.zeros(1, H, I, dtype=torch.bfloat16, device=DEV)
+    wd[0][:, hcols] = torch.randn(H, hcols.numel(), generator=g, device=DEV).bfloat16()
+    qd, sd = binding.quantize_fp8(wd, 128)
+    d = dict(x=x, ids=torch.zeros(T, 1, dtype=torch.int32, device=DEV), weights=torch.rand(T, 1, generator=g, device=DEV),
+             qgu=qgu.view(1, 2 * I, H), sgu=sgu.view(1, -1, 1), qd=qd, sd=sd)
+    assert all(int(c) % 128 == 0 for c in hcols[::128])  # whole groups of h: its 8-bit form is theirs alone
+    out = binding.experts_fp8(x, d["ids"], d["weights"], d["qgu"], d["sgu"], qd, sd)
+    wgu = torch.cat([qgu[p][hcols].double() * sgu[p, hcols // 128].double() for p in (0, 1)]).cpu().numpy()
+    check_columns(d, out, wgu, torch.arange(H, device=DEV), hcols)
