@@ -590,11 +590,14 @@ def shared_mlp_quant_fp8(x, q, scales, block_rows=1, stream=None):
 
 
 def quantize_fp8(x, block_rows=1, stream=None):
-    """Allocating form of shared_mlp_quant_fp8; returns q, scales."""
+    """Allocating form of shared_mlp_quant_fp8; returns q, scales (allocated for `stream`)."""
+    if stream is not None:
+        with _on(stream):
+            return quantize_fp8(x, block_rows)
     q = torch.empty(x.shape, dtype=FP8, device=x.device)
     rows = x.shape[-2] if block_rows == 1 else _blocks128(x.shape[-2])
     scales = torch.empty(*x.shape[:-2], rows, _blocks128(x.shape[-1]), dtype=torch.float32, device=x.device)
-    shared_mlp_quant_fp8(x, q, scales, block_rows, stream)
+    shared_mlp_quant_fp8(x, q, scales, block_rows)
     return q, scales
 
 

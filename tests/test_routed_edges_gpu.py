@@ -128,3 +128,20 @@ def test_experts_wide_intermediate():
     out = binding.experts_fp8(x, d["ids"], d["weights"], d["qgu"], d["sgu"], qd, sd)
     wgu = torch.cat([qgu[p][hcols].double() * sgu[p, hcols // 128].double() for p in (0, 1)]).cpu().numpy()
     check_columns(d, out, wgu, torch.arange(H, device=DEV), hcols)
+
+
+# ------------------------------------------------------------------ a caller's stream
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_on_any_stream(block_rows):
+    x = randn(gen(6), 300, 1040).to(DEV)
+    q, s = binding.quantize_fp8(x, block_rows)
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        q2, s2 = binding.quantize_fp8(x, block_rows, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+        # The memory belongs to that stream: the current one does not get it when it is freed.
+        at, n = q2.data_ptr(), q2.numel()
+        del q2, s2
+        assert torch.empty(n, dtype=torch.uint8, device=DEV).data_ptr() != at

@@ -28,3 +28,30 @@ def test_plans_stay_inside_the_workspace(tmp_path):
                UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
     r = subprocess.run([exe], capture_output=True, text=True, timeout=600, env=env)
     assert r.returncode == 0 and "all checks passed" in r.stdout, (r.stdout + r.stderr)[-4000:]
+
+
+def test_quantize_allocates_for_the_callers_stream(monkeypatch):
+    """Memory from the current stream's pool may still be in use there when the work on the
+    caller's stream starts, and is free for others as soon as the caller drops it."""
+    steps = []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            steps.append(("on", self.stream))
+
+        def __exit__(self, *_):
+            steps.append("off")
+
+    empty = torch.empty
+    monkeypatch.setattr(binding, "_on", On)
+    monkeypatch.setattr(binding, "shared_mlp_quant_fp8", lambda *a: steps.append("call"))
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (steps.append("empty"), empty(*a, **k))[1])
+    x = torch.zeros(3, 256, dtype=torch.bfloat16)
+    binding.quantize_fp8(x, stream=77)
+    assert steps == [("on", 77), "empty", "empty", "call", "off"]
+    steps.clear()
+    q, s = binding.quantize_fp8(x, 128)
+    assert steps == ["empty", "empty", "call"] and q.shape == (3, 256) and s.shape == (1, 2)
