@@ -117,9 +117,11 @@ int shared_mlp_workspace_bytes(int64_t M, int64_t H, int64_t I, int dtype, size_
  * with bf16 weights the two stages run as one launch whose down workgroups wait
  * (bounded) for the gate_up workgroups of the same launch; it keeps a few counters per
  * stream in a static device array (16 streams per GPU; further streams get the
- * two-launch form).  Calls on one stream, and on different streams, may run as usual;
- * two replays of one captured graph must not run at the same time (they share the
- * capturing stream's counters).  If a down workgroup ever gives up waiting, its output
+ * two-launch form).  Calls on one stream, and on different streams, may run as usual.  A
+ * captured launch keeps the counters of the stream it was captured on, wherever its graph
+ * is replayed: what was captured on one stream must not run at the same time as anything
+ * else captured on that stream or launched on it (a second replay of the same graph,
+ * another graph, an eager call).  The same holds for shared_mlp_linear (smlp_latent.h).  If a down workgroup ever gives up waiting, its output
  * rows are NaN.  A small fp32 layer (M * I <= 4096, M * H * I <= 2^20) runs both stages
  * in one single-workgroup launch with h in LDS; the workspace is still required.
  */
@@ -292,9 +294,11 @@ int shared_mlp_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t N, int x
  * 0 bytes are needed).  y must not overlap an input or the workspace.  M == 0 is a no-op.
  * Products are exact and summed in fp32, except where M > 32, K > 512 and y is bf16: there
  * the 8-bit matrix instructions are used, whose sum over a block of 128 is about 1.4e-5 off.
- * Like shared_mlp_linear, a product whose K is split over workgroups (few outputs) counts
- * arrivals per stream (16 streams per GPU; further ones run without the split), so two
- * replays of one captured graph must not run at the same time.
+ * A product whose K is split over workgroups (few outputs) counts arrivals in a static device
+ * array: on its stream's counters (16 streams per GPU; further ones run without the split),
+ * or, captured, on counters of its own (2^18 tiles per GPU over the life of the process;
+ * captures beyond that run without the split).  So graphs may be replayed beside one another
+ * and beside eager calls, as long as their buffers are apart; one graph not twice at a time.
  */
 int shared_mlp_linear_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* y,
                           int64_t M, int64_t K, int64_t N, int64_t ldy, int out_fp32, void* workspace,

@@ -62,6 +62,9 @@ int shared_mlp_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, size_t* b
  *              be NULL when that is 0); contents on entry ignored, on exit unspecified
  * y must not overlap x, w or the workspace; elements of y between row ends and the
  * next row (columns N .. ldy-1) are not written.  One or two kernels are enqueued.
+ * A K split counts its slices on counters of the stream, as shared_mlp_forward (smlp.h)
+ * does: what was captured on one stream must not run at the same time as anything else
+ * captured or launched on that stream.
  */
 int shared_mlp_linear(const void* x, const void* w, void* y, int64_t M, int64_t K, int64_t N,
                       int64_t ldy, int out_fp32, void* workspace, size_t workspace_bytes,

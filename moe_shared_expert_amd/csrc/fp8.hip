@@ -1850,8 +1850,8 @@ int launch_narrow_fp8(const F8Plan& p, const void* x, const void* w, const float
   a.g.ldo = (int)ldy;
   a.g.out_f32 = out_f32;
   const int cols = (int)((N + 16 * p.nt - 1) / (16 * p.nt));
-  a.arrived = p.ksplit > 1 ? reduce_counters(s, cols) : nullptr;
-  const int slices = a.arrived ? p.ksplit : 1;  // no counters left for this stream: no split
+  a.arrived = p.ksplit > 1 ? product_counters(s, cols) : nullptr;
+  const int slices = a.arrived ? p.ksplit : 1;  // no counters left: no split
   a.g.kslice = slices > 1 ? p.kslice : a.g.KB;
   a.g.part = part;
   const dim3 grid((unsigned)cols, (unsigned)slices);
@@ -1884,8 +1884,8 @@ int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t 
   const int tiles = (int)((M + p.bm - 1) / p.bm);
   F8Plan q = p;
   if (p.ksplit > 1) {
-    g.arrived = reduce_counters(s, (int)(tiles * ((N + p.bn - 1) / p.bn)));
-    if (!g.arrived) {  // no counters left for this stream: no split
+    g.arrived = product_counters(s, (int)(tiles * ((N + p.bn - 1) / p.bn)));
+    if (!g.arrived) {  // no counters left: no split
       q.ksplit = 1;
       q.kslice = g.KB;
     }

@@ -87,6 +87,19 @@ bool fusion_enabled();
 // Per-column counters for an in-launch K-split reduction over `columns` columns on
 // `stream`, or null (then a finalize launch reduces) (skinny.hip).
 uint32_t* reduce_counters(hipStream_t stream, int columns);
+// The same for a product whose launch may be captured: a captured launch keeps its counters
+// wherever and whenever its graph is replayed, so it gets `columns` of its own (null once they
+// are used up), any other launch its stream's (skinny.hip).
+uint32_t* product_counters(hipStream_t stream, int columns);
+// Counters given out once each: the first of n, or -1 when fewer are left of `all`.
+struct CounterRun {
+  int64_t used = 0;
+  int64_t take(int64_t n, int64_t all) {
+    if (n < 0 || n > all - used) return -1;
+    used += n;
+    return used - n;
+  }
+};
 bool decode_layer_eligible(const Plan& p);
 int launch_decode_layer(const Plan& p, const void* x, const void* w_gate_up, const void* w_down, void* out,
                         void* ws, int slot, int limit, hipStream_t s);

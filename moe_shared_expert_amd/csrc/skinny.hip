@@ -920,6 +920,34 @@ uint32_t* reduce_counters(hipStream_t s, int columns) {
   return base[dev] + (size_t)slot * kRedColumns * 16;
 }
 
+// Counters of captured launches, 16 words apart: never given back, because a graph may be
+// replayed for as long as the process lives.
+constexpr int64_t kCapturedCounters = 1 << 18;
+__device__ uint32_t g_captured_cnt[kCapturedCounters * 16];
+
+uint32_t* product_counters(hipStream_t s, int columns) {
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  // The null stream cannot be captured, and asking about it fails while another one is.
+  if (s && hipStreamIsCapturing(s, &status) != hipSuccess) {
+    (void)hipGetLastError();
+    return nullptr;
+  }
+  if (status == hipStreamCaptureStatusNone) return reduce_counters(s, columns);
+  if (!fusion_enabled()) return nullptr;
+  static std::mutex mu;
+  static uint32_t* base[64] = {};
+  static CounterRun run[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!base[dev] && hipGetSymbolAddress((void**)&base[dev], HIP_SYMBOL(g_captured_cnt)) != hipSuccess) {
+    base[dev] = nullptr;
+    return nullptr;
+  }
+  const int64_t at = run[dev].take(columns, kCapturedCounters);
+  return at < 0 ? nullptr : base[dev] + at * 16;
+}
+
 // Device address of this device's counter slots, looked up once per device.
 static int layer_sync_base(uint32_t** out) {
   static std::mutex mu;

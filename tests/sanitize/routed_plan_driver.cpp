@@ -126,9 +126,27 @@ static void linear_rows() {
     }
 }
 
+// Captured launches: no counter is handed out twice.
+static void captured_counters() {
+  std::snprintf(g_case, sizeof g_case, "captured counters");
+  smlp::CounterRun run;
+  int64_t end = 0;
+  for (int i = 0; i < 1000; ++i) {
+    const int64_t n = 1 + i * 7 % 128, at = run.take(n, 20000);
+    if (at < 0) {
+      require(end + n > 20000, "refused while enough are left");
+      continue;
+    }
+    require(at == end && at + n <= 20000, "handed out twice, or past the end");
+    end = at + n;
+  }
+  require(run.take(20001 - end, 20000) < 0 && run.take(-1, 20000) < 0, "past the end");
+}
+
 int main() {
   experts_regions();
   linear_rows();
+  captured_counters();
   std::printf(g_bad ? "%d checks failed\n" : "all checks passed\n", g_bad);
   return g_bad != 0;
 }

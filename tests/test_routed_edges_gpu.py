@@ -145,3 +145,57 @@ def test_quantize_on_any_stream(block_rows):
         at, n = q2.data_ptr(), q2.numel()
         del q2, s2
         assert torch.empty(n, dtype=torch.uint8, device=DEV).data_ptr() != at
+
+
+# ------------------------------------------------------------------ graphs side by side
+
+@pytest.mark.parametrize("size", [(16, 4096, 132), (64, 4096, 1000)])  # both kernels that split K
+def test_graphs_captured_on_one_stream_run_side_by_side(size):
+    M, K, N = size
+    cap, lanes = torch.cuda.Stream(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    need = max(256, binding.shared_mlp_linear_fp8_workspace_bytes(M, K, N, False))
+    jobs = []
+    for j in range(3):
+        g = gen(40 + j)
+        x = randn(g, M, K).bfloat16().to(DEV)
+        w, ws = binding.quantize_fp8(randn(g, N, K).to(DEV), 128)
+        jobs.append(dict(x=x, w=w, ws=ws, y=torch.empty(30, M, N, device=DEV),
+                         buf=torch.empty(need, dtype=torch.uint8, device=DEV)))
+
+    def products(job):
+        for y in job["y"]:
+            binding.shared_mlp_linear_fp8(job["x"], job["w"], job["ws"], y, workspace=job["buf"])
+
+    for job in jobs:
+        products(job)
+    torch.cuda.synchronize()
+    for job in jobs[:2]:
+        job["graph"] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(job["graph"], stream=cap):
+            products(job)
+    for job in jobs[:2]:
+        job["y"].fill_(float("nan"))
+        job["graph"].replay()
+        torch.cuda.synchronize()
+    with torch.cuda.stream(cap):
+        products(jobs[2])
+    torch.cuda.synchronize()
+    for job in jobs:
+        job["alone"] = job["y"][0].clone()
+        xq, xs = binding.quantize_fp8(job["x"])
+        x64 = xq.double() * xs.double().repeat_interleave(128, 1)
+        w64 = job["w"].double() * job["ws"].double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)
+        tol = (128 + K // 128 + 4) * U * (x64.abs() @ w64.abs().t())
+        assert bool(((job["alone"].double() - x64 @ w64.t()).abs() <= tol).all())
+    for _ in range(5):
+        for job in jobs:
+            job["y"].fill_(float("nan"))
+        torch.cuda.synchronize()
+        for job, lane in zip(jobs, lanes):
+            with torch.cuda.stream(lane):
+                job["graph"].replay()
+        with torch.cuda.stream(cap):
+            products(jobs[2])
+        torch.cuda.synchronize()
+        for job in jobs:
+            assert all(torch.equal(y, job["alone"]) for y in job["y"])
