@@ -1278,7 +1278,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
     const int lane = fresh(), ln = lane & 15, lg = lane >> 4;
     if constexpr (MODE == F8_LINEAR) {
       if (gridDim.y > 1) {
-        // K split over workgroups (one tile each, at most kReduceTiles): this slice's sums go
+        // K split over workgroups (one tile each, at most kCUs / 2): this slice's sums go
         // out agent-coherent as [slice][tile][row tile, column tile][lane][4]; the last slice
         // of a tile to arrive adds all of them in slice order and goes on with the sum.
         const uint32_t tile = blockIdx.x, per = BM * BN * 4, step = gridDim.x * per;

@@ -86,6 +86,7 @@ int stream_slot(hipStream_t stream);
 bool fusion_enabled();
 // Per-column counters for an in-launch K-split reduction over `columns` columns on
 // `stream`, or null (then a finalize launch reduces) (skinny.hip).
+constexpr int kRedColumns = 256;  // most columns
 uint32_t* reduce_counters(hipStream_t stream, int columns);
 // The same for a product whose launch may be captured: a captured launch keeps its counters
 // wherever and whenever its graph is replayed, so it gets `columns` of its own (null once they
@@ -159,8 +160,8 @@ constexpr int kCUs = 256;  // compute units the grids are sized for
 constexpr int kDownRun = 496, kTokenBlocks = 64, kTokenPairBlocks = 64;
 // Most pairs that one workgroup sorts, and most chunks otherwise.
 constexpr int kOneSort = 4096, kSortChunks = 64;
-// Most K slices of a projection, and most tiles (columns of workgroups) with a K split.
-constexpr int kSlices = 8, kReduceTiles = 256;
+// Most K slices of a projection.
+constexpr int kSlices = 8;
 
 // Whether `rows` rows of n 2-byte elements, ld apart, fit a buffer resource whose stores can be
 // dropped: an offset of 2^31 has to be past its end, so it spans at most 2^31 - 16 bytes.

@@ -77,6 +77,10 @@ struct LinearF8Plan {
   size_t x8_off, xs_off, part_off, workspace_bytes;
 };
 
+// Outputs of the one-launch projection of few rows, and tiles of a projection with a K split.
+constexpr int64_t kNarrowN = 1536, kSplitTiles = smlp::kCUs / 2;
+static_assert(kNarrowN / 16 <= smlp::kRedColumns && kSplitTiles <= smlp::kRedColumns, "a counter for each");
+
 int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, LinearF8Plan* out) {
   if (M < 0) return fail(SMLP_ERR_SHAPE, "M = %lld < 0", (long long)M);
   if (K < 16 || K % 16) return fail(SMLP_ERR_SHAPE, "K = %lld is not a positive multiple of 16", (long long)K);
@@ -90,7 +94,7 @@ int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, L
     p.f = stream_plan(M, KB);
     p.f.kind = smlp::F8_KIND_ROW;  // x is brought to its 8-bit form in each workgroup
     x_fp8 = 1;
-  } else if (M <= 16 && N <= 1536 && !x_fp8 && M * K < kLimit / 2) {
+  } else if (M <= 16 && N <= kNarrowN && !x_fp8 && M * K < kLimit / 2) {
     // Few rows of w: x is brought to its 8-bit form by the workgroups that use it (16 x 512 x
     // 7168: 6.8 us against 14 us with a launch of its own; at N = 2112 both take 14 us).
     p.f = stream_plan(M, KB);
@@ -118,7 +122,7 @@ int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, L
     const int b = t256 >= 256 ? 256 : t128 >= 256 ? 128 : 64;
     p.f = tile_plan(b, b, KB, exact);
     const int64_t tiles = ((M + b - 1) / b) * ((N + b - 1) / b);
-    if (b == 64 && 2 * tiles <= smlp::kCUs) {
+    if (b == 64 && tiles <= kSplitTiles) {
       // Not even one tile for every second compute unit: K over workgroups too, at least
       // eight blocks each (64 x 7168 x 7168: 20.6 -> 16.9 us; with more tiles or shorter
       // slices the second pass over the sums costs what the split saves).

@@ -901,7 +901,6 @@ int launch_skinny_gate_up(const Plan& p, const void* x, const void* w_gate_up, v
 
 // Per-column arrival counters of the in-launch K-split reduction: one block of
 // kRedColumns counters (16 words apart) per stream slot, per device.
-constexpr int kRedColumns = 256;
 __device__ uint32_t g_red_cnt[kLayerSyncSlots * kRedColumns * 16];
 
 uint32_t* reduce_counters(hipStream_t s, int columns) {
