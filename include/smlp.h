@@ -124,6 +124,8 @@ int shared_mlp_workspace_bytes(int64_t M, int64_t H, int64_t I, int dtype, size_
  * another graph, an eager call).  The same holds for shared_mlp_linear (smlp_latent.h).  If a down workgroup ever gives up waiting, its output
  * rows are NaN.  A small fp32 layer (M * I <= 4096, M * H * I <= 2^20) runs both stages
  * in one single-workgroup launch with h in LDS; the workspace is still required.
+ * SiLU(g) * u is formed as (g * u) / (1 + e^-g): a g * u past fp32's range gives an
+ * infinity or a NaN, also where SiLU(g) * u itself would be in it.
  */
 int shared_mlp_forward(const void* x, const void* w_gate_up, const void* w_down, void* out,
                        int64_t M, int64_t H, int64_t I, int dtype, int partial_fp32,

@@ -18,6 +18,10 @@ __device__ __forceinline__ uint32_t pack_fp8x4(float a, float b, float c, float 
   return (uint32_t)r;
 }
 
+// SiLU(g) * u in fp32, SiLU first: it is at most |g|, so only a result past the range of fp32
+// overflows (g * u formed first would, and be a NaN where e^-g does too).
+__device__ __forceinline__ float silu_then_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+
 // A 16x16x128 product of e4m3 operands, from zero.  Lane l holds 32 K elements of A row
 // l % 16 and of B column l % 16; any assignment of K elements to (l / 16, position) serves
 // as long as A and B use the same one.  Lane l, element j of the result: row

@@ -311,7 +311,7 @@ __global__ __launch_bounds__(WAVES * 64) void f8_stream_kernel(F8Args g) {
       f32x4 v = acc[t][m];
       if constexpr (GU) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = silu_mul(v[j], acc[t + FT][m][j]);
+        for (int j = 0; j < 4; ++j) v[j] = silu_then_mul(v[j], acc[t + FT][m][j]);
       }
       f8_store4(g, (size_t)(start + r), n, v);
     }
@@ -788,7 +788,7 @@ __global__ __launch_bounds__(256, 4) void f8_row_kernel(TokenArgs a) {
     for (int v2 = 1; v2 < WAVES; ++v2) s[q] += red[v2][q][threadIdx.x];
   }
   const int n = f0 + threadIdx.x;
-  if (GU) a.h[(size_t)blockIdx.y * a.I + n] = silu_mul(s[0], s[P - 1]);
+  if (GU) a.h[(size_t)blockIdx.y * a.I + n] = silu_then_mul(s[0], s[P - 1]);
   else if (a.out_f32) reinterpret_cast<float*>(a.out)[n] = s[0];
   else reinterpret_cast<uint16_t*>(a.out)[n] = (uint16_t)f2bf(s[0]);
 }
@@ -1327,7 +1327,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
         for (int j = 0; j < FT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float v = silu_mul(acc[i][j][e], acc[i][j + FT][e]);
+            const float v = silu_then_mul(acc[i][j][e], acc[i][j + FT][e]);
             acc[i][j][e] = v;
             mx = fmaxf(mx, fabsf(v));
           }

@@ -199,3 +199,30 @@ def test_graphs_captured_on_one_stream_run_side_by_side(size):
         torch.cuda.synchronize()
         for job in jobs:
             assert all(torch.equal(y, job["alone"]) for y in job["y"])
+
+
+# ------------------------------------------------------------------ SiLU(g) u where g u overflows
+
+@pytest.mark.parametrize("T", [1, 3, 100, 300])
+def test_experts_with_gate_times_up_past_the_range(T):
+    """Half of h is SiLU(-200) 2e36 = 0, the other SiLU(-30) 1e38 = -2.8e26 (less the 8-bit
+    rounding of the weights)."""
+    H, I = 256, 256
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    x[:, 0] = 1
+    wgu, wd = torch.zeros(2, I, H), torch.zeros(1, H, I)
+    half = torch.arange(I) >= I // 2
+    wgu[0, :, 0], wgu[1, :, 0] = torch.where(half, -30.0, -200.0), torch.where(half, 1e38, 2e36)
+    wd[0, 0, :I // 2] = 1
+    wd[0, 1, I // 2:] = 2.0 ** -6
+    qgu, sgu = binding.quantize_fp8(wgu.to(DEV), 128)
+    qd, sd = binding.quantize_fp8(wd.to(DEV), 128)
+    gate, up = [float(f64(qgu[p, I - 1, :1].cpu())[0] * sgu[p, 1, 0].item()) for p in (0, 1)]
+    ref = I // 2 * f64(qd[0, 1, -1:].cpu())[0] * sd[0, 0, 1].item() * (gate / (1 + np.exp(-gate)) * up)
+    for partial in (False, True):
+        out = binding.experts_fp8(x.to(DEV), torch.zeros(T, 1, dtype=torch.int32, device=DEV),
+                                  torch.ones(T, 1, device=DEV), qgu.view(1, 2 * I, H), sgu.view(1, 4, 2), qd, sd,
+                                  partial_fp32=partial).cpu().double()
+        assert bool((out[:, 0].abs() < 1e-30).all()) and bool((out[:, 2:] == 0).all())
+        # every h of the half is its group's largest: 448 times the scale, within fp32 roundings
+        assert bool(((out[:, 1] - ref).abs() <= 2.0 ** -7 * abs(ref)).all()), (out[:, 1], ref)
