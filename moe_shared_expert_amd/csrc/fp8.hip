@@ -1407,6 +1407,19 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
               for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(acc[i][j][e]));
             mx = fmaxf(mx, __shfl_xor(mx, 16));
             mx = fmaxf(mx, __shfl_xor(mx, 32));
+            // A result past the range stays an infinity; the exponent is the finite ones'.
+            if (__ballot(mx == INFINITY)) {
+              mx = 0.f;
+#pragma unroll
+              for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float v = fabsf(acc[i][j][e]);
+                  mx = fmaxf(mx, v < INFINITY ? v : 0.f);
+                }
+              mx = fmaxf(mx, __shfl_xor(mx, 16));
+              mx = fmaxf(mx, __shfl_xor(mx, 32));
+            }
             ex[i] = max(__float_as_uint(mx) >> 23, 15u);        // exponent field of the largest
             up = __uint_as_float((268u - ex[i]) << 23);         // brings it to [2^14, 2^15)
           }

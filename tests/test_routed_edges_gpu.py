@@ -226,3 +226,25 @@ def test_experts_with_gate_times_up_past_the_range(T):
         assert bool((out[:, 0].abs() < 1e-30).all()) and bool((out[:, 2:] == 0).all())
         # every h of the half is its group's largest: 448 times the scale, within fp32 roundings
         assert bool(((out[:, 1] - ref).abs() <= 2.0 ** -7 * abs(ref)).all()), (out[:, 1], ref)
+
+
+@pytest.mark.parametrize("T", [3, 1100])
+def test_experts_result_past_the_range_stays_in_its_column(T):
+    """One output column overflows to infinity; its neighbours (64 columns share an exponent
+    where y is held in fp16: 1100 rows of 4224) keep their values."""
+    H, I = 4224, 256
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    x[:, 0] = 1
+    wgu, wd = torch.zeros(1, 2 * I, H), torch.zeros(1, H, I)
+    wgu[0, :, 0] = 1          # h = SiLU(1) = 0.731 everywhere
+    wd[0, 5, :128], wd[0, 6, 128:], wd[0, 70, 128:] = 448.0, 1.0, -1.0
+    sgu, sd = torch.ones(1, 4, H // 128), torch.tensor([1e36, 1.0]).repeat(H // 128, 1)[None].contiguous()
+    out = binding.experts_fp8(x.to(DEV), torch.zeros(T, 1, dtype=torch.int32, device=DEV), torch.ones(T, 1, device=DEV),
+                              wgu.to(DEV).to(binding.FP8), sgu.to(DEV), wd.to(DEV).to(binding.FP8), sd.to(DEV))
+    out = out.cpu().double()
+    ref = 128 / (1 + np.exp(-1.0))
+    assert bool((out[:, 5] == float("inf")).all())
+    for col, sign in ((6, 1), (70, -1)):
+        assert bool(((out[:, col] - sign * ref).abs() <= 2.0 ** -7 * ref).all()), out[:, col]
+    out[:, [5, 6, 70]] = 0
+    assert bool((out == 0).all())
