@@ -8,6 +8,7 @@ the library to ``libsmlp.so`` and the module to ``_calls.so`` next to this file)
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -76,21 +77,27 @@ def _link_calls(obj: str) -> None:
     os.replace(tmp, CALLS)
 
 
+def _has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def build(verbose: bool = False) -> str:
+    """The library first: it needs hipcc alone.  The module needs g++ and torch's headers, and
+    is left out where torch is not installed (only the binding uses it)."""
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=8) as ex:
-        calls = ex.submit(_compile_calls)
+        calls = ex.submit(_compile_calls) if _has_torch() else None
         objs = list(ex.map(_compile, SOURCES))
-        calls_obj = calls.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", "-o", tmp, *objs, "--offload-arch=" + ARCH, "-Wl,-soname,libsmlp.so"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_calls(calls_obj)
+    if calls:
+        _link_calls(calls.result())
     if verbose:
-        print("built", LIB, "and", CALLS)
+        print("built", LIB, *(("and", CALLS) if calls else ("(torch is not installed: no _calls.so)",)))
     return LIB
 
 

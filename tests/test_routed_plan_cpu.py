@@ -55,3 +55,24 @@ def test_quantize_allocates_for_the_callers_stream(monkeypatch):
     steps.clear()
     q, s = binding.quantize_fp8(x, 128)
     assert steps == ["empty", "empty", "call"] and q.shape == (3, 256) and s.shape == (1, 2)
+
+
+def test_library_is_linked_without_the_python_module(tmp_path, monkeypatch):
+    """The C ABI needs hipcc alone: the module's compiler or headers may be missing."""
+    from moe_shared_expert_amd import build as b
+    monkeypatch.setattr(b, "BUILD", str(tmp_path / "objects"))
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "libsmlp.so"))
+    monkeypatch.setattr(b, "CALLS", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(b, "SOURCES", ["layout.cpp"])
+
+    def no_compiler():
+        raise RuntimeError("no compiler for the module")
+
+    monkeypatch.setattr(b, "_compile_calls", no_compiler)
+    with pytest.raises(RuntimeError, match="no compiler for the module"):
+        b.build()
+    assert os.path.exists(b.LIB) and not os.path.exists(b.CALLS)
+    # without torch there is nobody to use the module, and nothing to build it against
+    os.remove(b.LIB)
+    monkeypatch.setattr(b, "_has_torch", lambda: False, raising=False)
+    assert b.build() == b.LIB and os.path.exists(b.LIB) and not os.path.exists(b.CALLS)
