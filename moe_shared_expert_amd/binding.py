@@ -533,12 +533,21 @@ def _blocks128(n: int) -> int:
     return (n + 127) // 128
 
 
+def _int32(name, v):
+    """v as a C int (ctypes would drop its upper bits without a word)."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} = {v} is out of range")
+    return v
+
+
 @functools.lru_cache(maxsize=256)
 def _route_options(score, groups, top_groups, group_top, topk, renormalize, scale):
     if score not in ROUTE_SCORES:
         raise ValueError(f"score {score!r} is not one of {sorted(ROUTE_SCORES)}")
-    return _Route(ROUTE_SCORES[score], int(groups), int(groups if top_groups is None else top_groups), int(group_top),
-                  int(topk), int(bool(renormalize)), float(scale))
+    return _Route(ROUTE_SCORES[score], _int32("groups", groups),
+                  _int32("top_groups", groups if top_groups is None else top_groups), _int32("group_top", group_top),
+                  _int32("topk", topk), int(bool(renormalize)), float(scale))
 
 
 def shared_mlp_route(logits, ids, weights, score="sigmoid", bias=None, groups=1, top_groups=None, group_top=1,
@@ -576,6 +585,7 @@ def shared_mlp_quant_fp8(x, q, scales, block_rows=1, stream=None):
     parts, rows, cols = x.shape if x.dim() == 3 else (1, *x.shape)
     if not x.is_cuda or x.stride(-1) != 1 or (x.dim() == 3 and parts > 1 and x.stride(0) != rows * x.stride(1)):
         raise ValueError("x must be a GPU tensor of equally spaced rows with unit column stride")
+    block_rows = _int32("block_rows", block_rows)
     lead = (parts,) if x.dim() == 3 else ()
     qp = _want("q", q, FP8, x.shape)
     sp = _want("scales", scales, torch.float32,
@@ -585,7 +595,7 @@ def shared_mlp_quant_fp8(x, q, scales, block_rows=1, stream=None):
     ldx = x.stride(-2) if parts * rows > 1 else cols
     if rows == 0:
         return
-    _check(lib().shared_mlp_quant_fp8(x.data_ptr(), _dtype_code(x), parts, rows, cols, ldx, int(block_rows), qp, sp,
+    _check(lib().shared_mlp_quant_fp8(x.data_ptr(), _dtype_code(x), parts, rows, cols, ldx, block_rows, qp, sp,
                                       _queue(stream, dev)))
 
 

@@ -51,6 +51,19 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+// A C int: the library's options are narrower than Python's integers.
+int small_integer(PyObject* o, const char* name) {
+  const int64_t v = integer(o);
+  if (v != (int)v) throw Refused{std::string(name) + " = " + std::to_string(v) + " is out of range"};
+  return (int)v;
+}
+
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v != 0;
+}
+
 // Work and allocations go to the current stream (the binding makes a caller's stream current).
 hipStream_t queue(int dev) { return c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).stream(); }
 
@@ -102,15 +115,15 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[3] != Py_None) bias = static_cast<const float*>(want(tensor(a[3], "bias"), "bias", at::kFloat, {E}, dev));
     const double scale = PyFloat_AsDouble(a[8]);
     if (scale == -1.0 && PyErr_Occurred()) throw python_error();
-    const smlp_route r{(int)integer(a[2]), (int)integer(a[4]), (int)integer(a[5]), (int)integer(a[6]), (int)topk,
-                       (int)integer(a[7]), (float)scale};
+    const smlp_route r{small_integer(a[2], "score"), small_integer(a[4], "groups"), small_integer(a[5], "top_groups"),
+                       small_integer(a[6], "group_top"), (int)topk, truth(a[7]), (float)scale};
     at::Tensor ids = fresh({T, topk}, at::kInt, logits), weights = fresh({T, topk}, at::kFloat, logits);
     checked(shared_mlp_route(logits.data_ptr(), type == at::kFloat ? SMLP_FP32 : SMLP_BF16, T, E,
                              T > 1 ? logits.stride(0) : E, bias, &r, static_cast<int32_t*>(ids.data_ptr()),
                              static_cast<float*>(weights.data_ptr()), queue(dev)));
     PyObject* i = THPVariable_Wrap(std::move(ids));
     PyObject* w = THPVariable_Wrap(std::move(weights));
-    PyObject* both = PyTuple_Pack(2, i, w);
+    PyObject* both = i && w ? PyTuple_Pack(2, i, w) : nullptr;
     Py_XDECREF(i);
     Py_XDECREF(w);
     return both;
@@ -141,7 +154,7 @@ PyObject* linear_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t M = x.size(0), K = x.size(1), N = w.size(0), KB = blocks128(K);
     const int dev = x.is_cuda() ? x.get_device() : -1;
     const bool given = a[3] != Py_None;
-    const bool f32 = PyObject_IsTrue(a[4]) == 1;
+    const bool f32 = truth(a[4]);
     const void* xp = want(x, "x", given ? at::kFloat8_e4m3fn : at::kBFloat16, {M, K}, dev);
     const void* wp = want(w, "w", at::kFloat8_e4m3fn, {N, K}, dev);
     const float* wsp = static_cast<const float*>(want(tensor(a[2], "w_scales"), "w_scales", at::kFloat, {blocks128(N), KB}, dev));
@@ -165,7 +178,7 @@ PyObject* experts_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t T = x.size(0), H = x.size(1), E = wd.size(0), I = wd.size(2), topk = ids.size(1);
     const int64_t HB = blocks128(H), IB = blocks128(I);
     const int dev = x.is_cuda() ? x.get_device() : -1;
-    const bool f32 = PyObject_IsTrue(a[8]) == 1;
+    const bool f32 = truth(a[8]);
     const void* xp = want(x, "x", at::kBFloat16, {T, H}, dev);
     const void* ip = want(ids, "ids", at::kInt, {T, topk}, dev);
     const void* rp = want(tensor(a[2], "weights"), "weights", at::kFloat, {T, topk}, dev);

@@ -248,3 +248,28 @@ def test_experts_result_past_the_range_stays_in_its_column(T):
         assert bool(((out[:, col] - sign * ref).abs() <= 2.0 ** -7 * ref).all()), out[:, col]
     out[:, [5, 6, 70]] = 0
     assert bool((out == 0).all())
+
+
+# ------------------------------------------------------------------ arguments
+
+def test_route_options_past_32_bits_are_refused():
+    logits = randn(gen(1), 4, 64).to(DEV)
+    for kw in (dict(groups=2 ** 32 + 1), dict(top_groups=2 ** 32 + 1), dict(group_top=2 ** 32 + 1), dict(groups=-2 ** 32 + 1)):
+        with pytest.raises(ValueError):
+            binding.route(logits, 4, **kw)
+    # any truth value is one
+    a, b = binding.route(logits, 4, renormalize=2 ** 32), binding.route(logits, 4, renormalize=np.bool_(True))
+    c = binding.route(logits, 4)
+    assert torch.equal(a[1], c[1]) and torch.equal(b[1], c[1])
+    d, e = binding.route(logits, 4, renormalize=None), binding.route(logits, 4, renormalize=False)
+    assert torch.equal(d[1], e[1]) and not torch.equal(d[1], c[1])
+
+    class NoTruth:
+        def __bool__(self):
+            raise KeyError("no truth value")
+
+    with pytest.raises(KeyError):
+        binding.route(logits, 4, renormalize=NoTruth())
+    x = torch.zeros(2, 128, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(KeyError):
+        binding.linear_fp8(x, x.to(binding.FP8), torch.ones(1, 1, device=DEV), out_fp32=NoTruth())

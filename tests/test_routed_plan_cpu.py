@@ -76,3 +76,26 @@ def test_library_is_linked_without_the_python_module(tmp_path, monkeypatch):
     os.remove(b.LIB)
     monkeypatch.setattr(b, "_has_torch", lambda: False, raising=False)
     assert b.build() == b.LIB and os.path.exists(b.LIB) and not os.path.exists(b.CALLS)
+
+
+@pytest.mark.parametrize("name", ["groups", "top_groups", "group_top", "topk"])
+def test_route_options_past_32_bits_are_refused(name):
+    o = dict(score="sigmoid", groups=1, top_groups=1, group_top=1, topk=4, renormalize=True, scale=1.0)
+    for v in (2 ** 32 + 1, -2 ** 32 + 1, 2 ** 31):
+        with pytest.raises(ValueError):
+            binding._route_options(*{**o, name: v}.values())
+
+
+def test_quant_block_rows_past_32_bits_are_refused():
+    class Rows:  # stands for a GPU tensor: the check comes before anything is read
+        is_cuda, dtype, shape = True, torch.bfloat16, torch.Size((256, 128))
+
+        def dim(self):
+            return 2
+
+        def stride(self, i):
+            return (128, 1)[i]
+
+    for v in (2 ** 32 + 1, 2 ** 32 + 128, -2 ** 32 + 1):
+        with pytest.raises(ValueError, match="block_rows"):
+            binding.shared_mlp_quant_fp8(Rows(), None, None, v)
