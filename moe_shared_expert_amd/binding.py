@@ -583,7 +583,9 @@ def route(logits, topk: int, score="sigmoid", bias=None, groups=1, top_groups=No
 def shared_mlp_quant_fp8(x, q, scales, block_rows=1, stream=None):
     """8-bit form of x [rows, cols] or [parts, rows, cols] (bf16 or fp32, rows equally spaced)."""
     parts, rows, cols = x.shape if x.dim() == 3 else (1, *x.shape)
-    if not x.is_cuda or x.stride(-1) != 1 or (x.dim() == 3 and parts > 1 and x.stride(0) != rows * x.stride(1)):
+    # distance of the rows; that of the parts where they hold one row each
+    ldx = x.stride(-2) if rows > 1 else x.stride(0) if parts > 1 else cols
+    if not x.is_cuda or x.stride(-1) != 1 or (parts > 1 and rows and x.stride(0) != rows * ldx):
         raise ValueError("x must be a GPU tensor of equally spaced rows with unit column stride")
     block_rows = _int32("block_rows", block_rows)
     lead = (parts,) if x.dim() == 3 else ()
@@ -592,7 +594,6 @@ def shared_mlp_quant_fp8(x, q, scales, block_rows=1, stream=None):
                (*lead, rows if block_rows == 1 else _blocks128(rows), _blocks128(cols)))
     dev = x.get_device()
     _same_device(dev, q, scales)
-    ldx = x.stride(-2) if parts * rows > 1 else cols
     if rows == 0:
         return
     _check(lib().shared_mlp_quant_fp8(x.data_ptr(), _dtype_code(x), parts, rows, cols, ldx, block_rows, qp, sp,

@@ -273,3 +273,16 @@ def test_route_options_past_32_bits_are_refused():
     x = torch.zeros(2, 128, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(KeyError):
         binding.linear_fp8(x, x.to(binding.FP8), torch.ones(1, 1, device=DEV), out_fp32=NoTruth())
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_parts_of_one_row(block_rows):
+    """Parts of one row: their distance is the rows' distance, whatever the unused row stride is."""
+    base = randn(gen(11), 6, 4, 272).to(DEV)
+    for x in (base[:, 2:3], base[:, 1].unsqueeze(1), base[2].unsqueeze(0).transpose(0, 1), base[:1, :1]):
+        assert x.shape[1] == 1 and x.stride(-1) == 1
+        q, s = binding.quantize_fp8(x, block_rows)
+        q2, s2 = binding.quantize_fp8(x.contiguous(), block_rows)
+        assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+    q, s = binding.quantize_fp8(base[:, :0], block_rows)
+    assert q.shape == (6, 0, 272) and s.shape == (6, 0, 3)
