@@ -286,3 +286,80 @@ def test_quantize_parts_of_one_row(block_rows):
         assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
     q, s = binding.quantize_fp8(base[:, :0], block_rows)
     assert q.shape == (6, 0, 272) and s.shape == (6, 0, 3)
+
+
+# ------------------------------------------------------------------ y held in fp16
+
+def quantized64(x):
+    """What the 8-bit form of x stands for (fp64; the scale and the scaled value are fp32 numbers)."""
+    rows, cols = x.shape
+    pad = torch.nn.functional.pad(x.float(), (0, -cols % 128)).view(rows, -1, 128)
+    a = pad.abs().amax(2, keepdim=True).clamp_min(1e-30)
+    q = (pad * (448.0 * (1.0 / a))).to(binding.FP8)
+    s = a / 448.0
+    return (q.double() * s.double()).view(rows, -1)[:, :cols], s.double().expand(-1, -1, 128).reshape(rows, -1)[:, :cols]
+
+
+def experts64(d, first=0):
+    """Output, sum of absolute products, largest change by one flip of h per pair, and sum of the
+    pairs' magnitudes, in fp64 on the GPU."""
+    E, H, I = d["qd"].shape
+    nb = routed.blocks(I)
+
+    def blocks(q, s):
+        return q.double() * s.double().repeat_interleave(128, 0)[:q.shape[0]].repeat_interleave(128, 1)[:, :q.shape[1]]
+
+    x = quantized64(d["x"])[0]
+    out, size, flip, parts = (torch.zeros(x.shape, dtype=torch.float64, device=DEV) for _ in range(4))
+    for e in range(E):
+        t, j = (d["ids"] == e + first).nonzero(as_tuple=True)
+        if not t.numel():
+            continue
+        g = x[t] @ blocks(d["qgu"][e, :I], d["sgu"][e, :nb]).t().contiguous()
+        u = x[t] @ blocks(d["qgu"][e, I:], d["sgu"][e, nb:]).t().contiguous()
+        h, s = quantized64(g / (1 + torch.exp(-g)) * u)
+        w = blocks(d["qd"][e], d["sd"][e])
+        p = d["weights"][t, j, None].double()
+        y = p * (h @ w.t().contiguous())
+        out.index_add_(0, t, y)
+        parts.index_add_(0, t, y.abs())
+        size.index_add_(0, t, p * (h.abs() @ w.abs().t().contiguous()))
+        step = torch.maximum(h.abs() / 8, s * 2.0 ** -9)
+        flip.index_add_(0, t, p * torch.cat([(w.abs() * r).amax(1)[None] for r in step]))
+    return out, size, flip, parts
+
+
+@pytest.mark.parametrize("partial", [False, True])
+@pytest.mark.parametrize("size", [(600, 2000, 336, 24, 40, 4, 8),   # tiles of 64 rows, an H that is no multiple of 64,
+                                  (301, 7168, 384, 24, 24, 4, 0),   # other ranks' experts
+                                  (2048, 1040, 208, 8, 9, 2, 1)])   # tiles of 256 rows
+def test_experts_of_many_pairs(size, partial):
+    """Sizes whose y passes through fp16 where out is bf16, every second row of w_down 64 times
+    smaller than its neighbours.
+
+    Errors, relative and rms: rounding to bf16 1.66e-3 (half a unit, spread over the mantissas);
+    g and u through the 8-bit instruction are about 1.4e-5 off, h 2e-5, which moves a share of
+    2e-5 / spacing of its values by one spacing (0.09 of the value): sqrt(0.8 * 2e-5 * 0.09) =
+    1.2e-3; y in fp16 2e-4.  Together 2.1e-3 (y in bf16 instead of fp16: 2.6e-3).  In fp32: h
+    some 5e-7 off (sums and exponential), so 1.9e-4.  Per output: fp32 sums as elsewhere, the
+    8-bit instruction's 1.8e-5 for the products and twice for h's scale, three flips per pair
+    (0.1 are expected)."""
+    T, H, I, E, every, k, first = size
+    d = make_experts(700 + T, T, H, I, E, k, every)
+    wd = randn(gen(T), E, H, I) / I ** 0.5
+    wd[:, 1::2] /= 64
+    d["qd"], d["sd"] = binding.quantize_fp8(wd.to(DEV), 128)
+    rows = T * k / min(T * k, E)
+    assert rows > 12 and T * k * H > 4 << 20
+    out = binding.experts_fp8(d["x"], d["ids"], d["weights"], d["qgu"], d["sgu"], d["qd"], d["sd"], first_expert=first,
+                              partial_fp32=partial).double()
+    ref, size_, flip, parts = experts64(d, first)
+    nb = routed.blocks(I)
+    tol = (128 + nb + k + 8) * U * size_ + (2 if partial else 3) * flip + 1e-30
+    if not partial:
+        tol += 3 * 1.8e-5 * size_ + 2.0 ** -8 * ref.abs() + 1.01 * 2.0 ** -11 * parts
+    err = (out - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    for half in (0, 1):
+        rel = float(err[:, half::2].norm() / ref[:, half::2].norm())
+        assert rel <= (5e-4 if partial else 2.4e-3), (half, rel)
