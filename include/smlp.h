@@ -295,7 +295,9 @@ int shared_mlp_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t N, int x
  * 16-byte aligned, y aligned to its element; workspace 256-byte aligned (may be NULL when
  * 0 bytes are needed).  y must not overlap an input or the workspace.  M == 0 is a no-op.
  * Products are exact and summed in fp32, except where M > 32, K > 512 and y is bf16: there
- * the 8-bit matrix instructions are used, whose sum over a block of 128 is about 1.4e-5 off.
+ * the 8-bit matrix instructions are used at twice the rate, whose sums are about 1.5e-5 off
+ * (2-norm; one bf16 value in about 500 rounds the other way for it).  out_fp32 == 1 always
+ * takes the exact products.
  * A product whose K is split over workgroups (few outputs) counts arrivals in a static device
  * array: on its stream's counters (16 streams per GPU; further ones run without the split),
  * or, captured, on counters of its own (2^18 tiles per GPU over the life of the process;
@@ -326,6 +328,12 @@ int shared_mlp_experts_fp8_workspace_bytes(int64_t T, int64_t H, int64_t I, int6
  *   w_down      e4m3 [E, H, I], s_down [E, ceil(H / 128), ceil(I / 128)]
  *   out         [T, H] bf16 (rounded once; with many tokens each expert's y passes through
  *               fp16 with a common exponent per 64 columns) or fp32 (partial_fp32 != 0)
+ * With at most 12 pairs per expert on average, and with partial_fp32 != 0, products are exact
+ * and summed in fp32.  Otherwise the 8-bit matrix instructions are used: g and u are about
+ * 1.5e-5 off (2-norm), so one value of h in some thousands is stored as the neighbouring e4m3
+ * value, and out is 2.0e-3 to 2.3e-3 off the definition instead of the 1.7e-3 that rounding
+ * to bf16 alone makes.  partial_fp32 != 0 is how a caller has the exact products (8192 tokens,
+ * 8 of 64 experts of 768: 2.98 ms instead of 1.52).
  *   workspace   >= shared_mlp_experts_fp8_workspace_bytes(...), 256-byte aligned
  * H and I positive multiples of 16; E in [1, SMLP_MAX_EXPERTS]; topk in [1, SMLP_MAX_TOPK];
  * T * H, T * topk, T * topk * I and 2 * I * H < 2^31; x, w_gate_up, w_down and out 16-byte

@@ -96,7 +96,8 @@ int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, L
     x_fp8 = 1;
   } else if (M <= 16 && N <= kNarrowN && !x_fp8 && M * K < kLimit / 2) {
     // Few rows of w: x is brought to its 8-bit form by the workgroups that use it (16 x 512 x
-    // 7168: 6.8 us against 14 us with a launch of its own; at N = 2112 both take 14 us).
+    // 7168: 6.8 us against 14 us with a launch of its own; at N = 2112 they took the same, 11.7 us
+    // with the launch, of which it is 2.5).
     p.f = stream_plan(M, KB);
     p.f.kind = smlp::F8_KIND_NARROW;
     p.f.nt = 1;
@@ -115,17 +116,18 @@ int make_linear_plan(int64_t M, int64_t K, int64_t N, int x_fp8, int out_fp32, L
     p.f = stream_plan(M, KB);
   } else {
     const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256), t128 = blocks128(M) * blocks128(N);
-    // fp32 results and sums over few blocks go through the bf16 instructions: the 8-bit ones
-    // are 1.4e-5 of a block's sum off, which bf16 results do not show once several blocks
-    // average it, and with a short K the time is in the stores.
+    // fp32 results go through the bf16 instructions, since the 8-bit ones are 1.5e-5 off (8192 x
+    // 7168 x 6144 706 us against 325 us for a bf16 result), and so do short K, where the time is
+    // in the stores.
     const int exact = out_fp32 || KB <= 4;
     const int b = t256 >= 256 ? 256 : t128 >= 256 ? 128 : 64;
     p.f = tile_plan(b, b, KB, exact);
     const int64_t tiles = ((M + b - 1) / b) * ((N + b - 1) / b);
     if (b == 64 && tiles <= kSplitTiles) {
       // Not even one tile for every second compute unit: K over workgroups too, at least
-      // eight blocks each (64 x 7168 x 7168: 20.6 -> 16.9 us; with more tiles or shorter
-      // slices the second pass over the sums costs what the split saves).
+      // eight blocks each.  A K step takes 0.33 us and the join of the slices' sums 2.2 us, so
+      // short slices gain little (e4m3 x, bf16 y; without and with the split: 333 x 1000 x 2000
+      // 9.9 and 9.4 us, 64 x 7168 x 7168 22.9 and 16.1 us, 64 x 2112 x 7168 22.7 and 12.2 us).
       int64_t slices = 2 * smlp::kCUs / tiles;
       if (slices > KB / 8) slices = KB / 8;
       if (slices > smlp::kSlices) slices = smlp::kSlices;
@@ -167,6 +169,8 @@ int make_experts_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, 
   p.topk = topk;
   p.P = T * topk;
   const int64_t HB = blocks128(H), IB = blocks128(I);
+  // Rows per expert as if every pair were of an expert held here: a rank of an expert-parallel
+  // group plans for more rows than it has.
   const int64_t active = p.P < E ? p.P : E;
   const int64_t rows = active ? p.P / active : 0;
   // Streaming against tiles of 64 rows, the same experts: 8 rows per expert 198 and 235 us, 16
