@@ -32,6 +32,7 @@ namespace smlp {
 namespace {
 
 enum { F8_LINEAR = 0, F8_GATE_UP = 1, F8_DOWN = 2 };
+constexpr int kGuarded = 2;  // F8Args::out_f32
 
 struct F8Args {
   const uint8_t* a;    // activations [rows, K]
@@ -54,8 +55,8 @@ struct F8Args {
   void* out;           // projection: y; gate_up: h; down: y (rows: sorted positions)
   int ldo;
   int out_f32;         // fp32 (1) or bf16 (0) output; gate_up: fp32 h (1) or e4m3 h (0); down:
-                       // fp32 y (1) or fp16 y with exponents (0)
-  int by_rows;         // tiled projection with bf16 y: full tiles store whole rows through a buffer
+                       // fp32 y (1) or fp16 y with exponents (0); tiled projection: kGuarded for
+                       // bf16 rows that do not fit a buffer
   float* hs;           // gate_up with e4m3 h: scales, block b of position p at hs[b * hs_ld + p]
   int hs_ld;
   uint8_t* yexp;       // down with fp16 y: exponent of position p and columns 64 c .. + 63 at
@@ -111,7 +112,7 @@ __device__ __forceinline__ void f8_barrier() {
 // Store four consecutive features n .. n+3 of one output row.
 __device__ __forceinline__ void f8_store4(const F8Args& g, size_t row, int n, f32x4 v) {
   const size_t at = row * (size_t)g.ldo + n;
-  if (g.out_f32) {
+  if (g.out_f32 & 1) {
     float* p = reinterpret_cast<float*>(g.out) + at;
     if (n + 3 < g.N && ((uintptr_t)p & 15) == 0) {
       *reinterpret_cast<f32x4*>(p) = v;
@@ -1392,7 +1393,9 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args g) {
       stores = (TM + 3) / 4 + TM / 2;
     } else {
       constexpr int CPR = 2 * TN, RPI = 64 / CPR;  // 16-byte chunks per staged row, rows per store
-      const bool whole = MODE == F8_DOWN ? !g.out_f32 : g.by_rows && cur.f0 + FN <= g.N;
+      const bool whole = MODE == F8_DOWN
+                             ? !g.out_f32
+                             : !g.out_f32 && cur.f0 + FN <= g.N && g.ldo % 8 == 0 && ((uintptr_t)g.out & 15) == 0;
       if (whole) {
         // Rows through LDS: a lane's four features are 8 bytes of 16 different rows, the
         // stores below whole runs of 32 TN bytes per row.  Projection: bf16.  Experts: fp16
@@ -1898,7 +1901,7 @@ int launch_linear_fp8(const F8Plan& p, const void* a8, const float* as, int64_t 
   g.out = y;
   g.ldo = (int)ldy;
   g.out_f32 = out_f32;
-  g.by_rows = p.by_rows && !out_f32 && ldy % 8 == 0 && (uintptr_t)y % 16 == 0;
+  if (p.kind == F8_KIND_TILE && !out_f32 && !p.by_rows) g.out_f32 = kGuarded;
   g.part = part;
   const int tiles = (int)((M + p.bm - 1) / p.bm);
   F8Plan q = p;
