@@ -25,6 +25,7 @@
  *    call returns and allocates no device memory.
  *  - Work is enqueued on `stream` (0 = the legacy default stream) and the call
  *    returns without synchronising.  The library never synchronises a stream.
+ *    The GPU of the stream and the buffers must be the current one (hipSetDevice).
  *  - Return value: SMLP_OK (0) or an error status.  On any error nothing was
  *    launched; shared_mlp_last_error() gives a detail string (thread-local).
  *    Argument validation happens on the host before any HIP call, so every

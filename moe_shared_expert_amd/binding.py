@@ -10,6 +10,7 @@ HIP runtime torch already loaded (one runtime per process).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -511,13 +512,30 @@ def _queue(stream, index):
     """Raw handle of `stream`, or of the current stream of GPU `index`."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if not hasattr(stream, "cuda_stream"):
+        return int(stream)
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
+    return stream.cuda_stream
 
 
-def _on(stream):
-    """Context in which torch allocates for `stream`, so that scratch memory freed when a call
-    returns is reused only behind the work that uses it."""
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+def _gpu(index):
+    """Context in which GPU `index` is the current one: launches on a default stream go to the
+    current GPU, and the library looks counters up for it."""
+    return _nothing if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+
+
+_nothing = contextlib.nullcontext()
+
+
+def _on(stream, device):
+    """Context in which torch allocates for `stream` of the tensors' GPU, so that scratch memory
+    freed when a call returns is reused only behind the work that uses it."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _scratch(need, device, stream):
@@ -525,7 +543,7 @@ def _scratch(need, device, stream):
         return None
     if stream is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
-    with _on(stream):
+    with _on(stream, device):
         return torch.empty(need, dtype=torch.uint8, device=device)
 
 
@@ -560,10 +578,10 @@ def shared_mlp_route(logits, ids, weights, score="sigmoid", bias=None, groups=1,
     r = _route_options(score, groups, top_groups, group_top, topk, renormalize, scale)
     dev = logits.get_device()
     _same_device(dev, ids, weights, bias)
-    rc = lib().shared_mlp_route(src, _dtype_code(logits), T, E, ldl,
-                                None if bias is None else _want("bias", bias, torch.float32, (E,)), r,
-                                _want("ids", ids, torch.int32, (T, topk)),
-                                _want("weights", weights, torch.float32, (T, topk)), _queue(stream, dev))
+    args = (src, _dtype_code(logits), T, E, ldl, None if bias is None else _want("bias", bias, torch.float32, (E,)), r,
+            _want("ids", ids, torch.int32, (T, topk)), _want("weights", weights, torch.float32, (T, topk)))
+    with _gpu(dev):
+        rc = lib().shared_mlp_route(*args, _queue(stream, dev))
     if rc:
         _check(rc)
 
@@ -572,7 +590,7 @@ def route(logits, topk: int, score="sigmoid", bias=None, groups=1, top_groups=No
           scale=1.0, stream=None):
     """Allocating form of shared_mlp_route; returns ids, weights (allocated for `stream`)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, logits.device):
             return route(logits, topk, score, bias, groups, top_groups, group_top, renormalize, scale)
     if score not in ROUTE_SCORES:
         raise ValueError(f"score {score!r} is not one of {sorted(ROUTE_SCORES)}")
@@ -596,14 +614,17 @@ def shared_mlp_quant_fp8(x, q, scales, block_rows=1, stream=None):
     _same_device(dev, q, scales)
     if rows == 0:
         return
-    _check(lib().shared_mlp_quant_fp8(x.data_ptr(), _dtype_code(x), parts, rows, cols, ldx, block_rows, qp, sp,
-                                      _queue(stream, dev)))
+    with _gpu(dev):
+        rc = lib().shared_mlp_quant_fp8(x.data_ptr(), _dtype_code(x), parts, rows, cols, ldx, block_rows, qp, sp,
+                                        _queue(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def quantize_fp8(x, block_rows=1, stream=None):
     """Allocating form of shared_mlp_quant_fp8; returns q, scales (allocated for `stream`)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x.device):
             return quantize_fp8(x, block_rows)
     q = torch.empty(x.shape, dtype=FP8, device=x.device)
     rows = x.shape[-2] if block_rows == 1 else _blocks128(x.shape[-2])
@@ -639,8 +660,9 @@ def shared_mlp_linear_fp8(x, w, w_scales, y, x_scales=None, workspace=None, stre
         need = shared_mlp_linear_fp8_workspace_bytes(M, K, N, quantized)
         workspace = _scratch(need, x.device, stream)
     _same_device(dev, x_scales, w, w_scales, y, workspace)
-    rc = lib().shared_mlp_linear_fp8(xp, xsp, wp, wsp, yp, M, K, N, ldy, out_fp32, _ptr(workspace),
-                                     _ws_bytes(workspace), _queue(stream, dev))
+    with _gpu(dev):
+        rc = lib().shared_mlp_linear_fp8(xp, xsp, wp, wsp, yp, M, K, N, ldy, out_fp32, _ptr(workspace),
+                                         _ws_bytes(workspace), _queue(stream, dev))
     if rc:
         _check(rc)
     return y
@@ -649,7 +671,7 @@ def shared_mlp_linear_fp8(x, w, w_scales, y, x_scales=None, workspace=None, stre
 def linear_fp8(x, w, w_scales, x_scales=None, out_fp32=False, workspace=None, stream=None):
     """Allocating form of shared_mlp_linear_fp8 (y and any workspace allocated for `stream`)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x.device):
             return linear_fp8(x, w, w_scales, x_scales, out_fp32, workspace)
     return (_calls or _load_calls()).linear_fp8(x, w, w_scales, x_scales, out_fp32, workspace)
 
@@ -681,8 +703,9 @@ def shared_mlp_experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down
         need = shared_mlp_experts_fp8_workspace_bytes(T, H, I, E, topk, partial)
         workspace = _scratch(max(need, 256), x.device, stream)
     _same_device(dev, ids, weights, w_gate_up, s_gate_up, w_down, s_down, out, workspace)
-    rc = lib().shared_mlp_experts_fp8(*args, T, H, I, E, topk, first_expert, partial, _ptr(workspace),
-                                      _ws_bytes(workspace), _queue(stream, dev))
+    with _gpu(dev):
+        rc = lib().shared_mlp_experts_fp8(*args, T, H, I, E, topk, first_expert, partial, _ptr(workspace),
+                                          _ws_bytes(workspace), _queue(stream, dev))
     if rc:
         _check(rc)
     return out
@@ -692,7 +715,7 @@ def experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_exp
                 workspace=None, stream=None):
     """Allocating form of shared_mlp_experts_fp8 (out and any workspace allocated for `stream`)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x.device):
             return experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert, partial_fp32,
                                workspace)
     return (_calls or _load_calls()).experts_fp8(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert,

@@ -36,7 +36,7 @@ def test_quantize_allocates_for_the_callers_stream(monkeypatch):
     steps = []
 
     class On:
-        def __init__(self, stream):
+        def __init__(self, stream, device):
             self.stream = stream
 
         def __enter__(self):
@@ -99,3 +99,84 @@ def test_quant_block_rows_past_32_bits_are_refused():
     for v in (2 ** 32 + 1, 2 ** 32 + 128, -2 ** 32 + 1):
         with pytest.raises(ValueError, match="block_rows"):
             binding.shared_mlp_quant_fp8(Rows(), None, None, v)
+
+
+class FakeTensor:
+    """Stands for a tensor of GPU 1 (nothing reads it)."""
+    is_cuda, device = True, torch.device("cuda:1")
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape = dtype, torch.Size(shape)
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        st = [1]
+        for n in reversed(self.shape[1:]):
+            st.insert(0, st[0] * n)
+        return st if i is None else st[i]
+
+    def get_device(self):
+        return 1
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x1000
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return 1
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_run_with_the_tensors_gpu_current(monkeypatch, current):
+    """A default stream's handle names no GPU: a launch on it goes to the current one."""
+    now, seen = [current], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: (seen.append((name, now[0])), 0)[1]
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
+    monkeypatch.setattr(binding, "lib", Library)
+    f = FakeTensor
+    bf, f32, i32, f8 = torch.bfloat16, torch.float32, torch.int32, binding.FP8
+    buf = f(torch.uint8, 1 << 20)
+    binding.shared_mlp_route(f(f32, 4, 64), f(i32, 4, 2), f(f32, 4, 2))
+    binding.shared_mlp_quant_fp8(f(bf, 4, 128), f(f8, 4, 128), f(f32, 4, 1))
+    binding.shared_mlp_linear_fp8(f(bf, 4, 128), f(f8, 64, 128), f(f32, 1, 1), f(bf, 4, 64), workspace=buf)
+    binding.shared_mlp_experts_fp8(f(bf, 4, 128), f(i32, 4, 2), f(f32, 4, 2), f(f8, 2, 256, 128), f(f32, 2, 2, 1),
+                                   f(f8, 2, 128, 128), f(f32, 2, 1, 1), f(bf, 4, 128), workspace=buf)
+    assert [g for _, g in seen] == [1] * 4 and len({n for n, _ in seen}) == 4 and now == [current]
+
+
+def test_a_stream_of_another_gpu_is_refused(monkeypatch):
+    class Stream:
+        cuda_stream, device = 0x77, torch.device("cuda:0")
+
+    x = FakeTensor(torch.bfloat16, 4, 128)
+    ids, weights = FakeTensor(torch.int32, 4, 2), FakeTensor(torch.float32, 4, 2)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    for call in (lambda: binding.shared_mlp_route(x, ids, weights, stream=Stream()),
+                 lambda: binding.route(x, 2, stream=Stream()), lambda: binding.quantize_fp8(x, stream=Stream()),
+                 lambda: binding.linear_fp8(x, x, x, stream=Stream()),
+                 lambda: binding.experts_fp8(x, x, x, x, x, x, x, stream=Stream())):
+        with pytest.raises(ValueError, match="stream"):
+            call()
